@@ -22,6 +22,9 @@ The two-level formats (NVFP4, the uniform grid, the cut E2M1) also take
 double-block scales (``outer=True``): one FP32 outer scale per 128 elements
 of each row of the quantized operand instead of the tensor scale.
 
+The 4-bit KV cache (``KVCache``, ``KVBatch``, ``kv_append``, ``kv_attention``,
+...) is in the submodule ``kv``; its names are this package's too.
+
 ``stream`` (every call): None launches on torch's current stream; a
 ``torch.cuda.Stream`` launches on it, and whatever the call allocates
 (outputs, the workspace, an uploaded tensor scale) is allocated with that
@@ -64,7 +67,10 @@ STATUS = {0: "FP4_OK", -1: "FP4_ERR_NULL", -2: "FP4_ERR_FORMAT", -3: "FP4_ERR_SH
 # every symbol include/fp4.h declares
 EXPORTS = ("fp4_workspace_bytes", "fp4_quantize", "fp4_dequantize", "fp4_rht",
            "fp4_rht_signs", "fp4_status_str", "fp4_workspace_bytes_dual", "fp4_quantize_dual",
-           "fp4_gemm_mx", "fp4_quantize_noalloc", "fp4_quantize_input_bytes")
+           "fp4_gemm_mx", "fp4_quantize_noalloc", "fp4_quantize_input_bytes",
+           "fp4_kv_append", "fp4_kv_gather", "fp4_kv_attention",
+           "fp4_kv_attention_workspace_bytes", "fp4_kv_copy_pages", "fp4_kv_fork",
+           "fp4_kv_free", "fp4_kv_compact")
 
 
 class FP4Error(RuntimeError):
@@ -119,6 +125,7 @@ def load():
         L.fp4_rht.restype = i32
         L.fp4_gemm_mx.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, i64, vp]
         L.fp4_gemm_mx.restype = i32
+        kv.bind(L)
         L.fp4_rht_signs.argtypes = [ctypes.c_uint64]
         L.fp4_rht_signs.restype = ctypes.c_uint16
         L.fp4_status_str.argtypes = [i32]
@@ -489,3 +496,9 @@ def rht(x: torch.Tensor, axis: str = "row", seed: int = 0, inverse: bool = False
     if st != FP4_OK:
         raise FP4Error(st, "fp4_rht")
     return out
+
+
+from block_scaled_bit_fp4_amd import kv  # noqa: E402  (it uses the names above)
+from block_scaled_bit_fp4_amd.kv import (  # noqa: E402,F401
+    KVBatch, KVCache, kv_append, kv_attention, kv_attention_workspace_bytes, kv_compact,
+    kv_copy_pages, kv_fork, kv_free, kv_gather, new_kv_cache)

@@ -464,6 +464,8 @@ fp4_status fp4_gemm_mx(const uint8_t* a_codes, const uint8_t* a_scales,
 
 }  // extern "C"
 
+int32_t fp4_launch_status(hipError_t e, hipStream_t s) { return finish(e, s); }
+
 hipError_t fp4_launch_quantize(const QuantLaunch& q, hipStream_t s) {
   switch (q.format) {
     case FP4_NVFP4: return fp4_launch_quantize_nvfp4(q, s);

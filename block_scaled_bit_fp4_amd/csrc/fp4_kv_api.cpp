@@ -1,0 +1,337 @@
+// fp4_kv_api.cpp -- the C ABI of the 4-bit KV cache (include/fp4.h): every
+// argument is checked on the host before any HIP call.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "fp4.h"
+#include "fp4_kv.h"
+#include "fp4_kv_pages.h"
+#include "fp4_launch.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// A stride of `elements` of `size` bytes that keeps 16-byte alignment.
+bool stride16(int64_t elements, int64_t size) { return (elements * size) % 16 == 0; }
+
+int log2_of(int32_t v) {
+  int n = 0;
+  while ((1 << n) < v) ++n;
+  return n;
+}
+
+int32_t block_of(const fp4_kv_cache* c) { return c->format == FP4_NVFP4 ? 16 : 32; }
+
+fp4_status check_geometry(const fp4_kv_cache* c) {
+  if (!c) return FP4_ERR_NULL;
+  if (c->format != FP4_NVFP4 && c->format != FP4_MXFP4 && c->format != FP4_MXFP4_OAS)
+    return FP4_ERR_FORMAT;
+  if (c->rht != 0 && c->rht != 1) return FP4_ERR_FORMAT;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return FP4_ERR_SHAPE;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return FP4_ERR_SHAPE;
+  if (c->layers < 1 || c->heads < 1 || c->heads > 1024) return FP4_ERR_SHAPE;
+  if (c->pages < 1 || c->pages > 0x7FFFFFFFll) return FP4_ERR_SHAPE;
+  return FP4_OK;
+}
+
+fp4_status check_arrays(const fp4_kv_cache* c, bool factors) {
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return FP4_ERR_NULL;
+  if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) ||
+      !aligned(c->v_scales, 16))
+    return FP4_ERR_ALIGN;
+  if (factors && c->format == FP4_NVFP4) {
+    if (!c->k_scale || !c->v_scale) return FP4_ERR_NULL;
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return FP4_ERR_ALIGN;
+  }
+  return FP4_OK;
+}
+
+// Shape of a batch; the pointers too if `pointers`.
+fp4_status check_batch(const fp4_kv_cache* c, const fp4_kv_batch* b, int64_t tokens,
+                       bool pointers) {
+  if (!b) return FP4_ERR_NULL;
+  if (b->batch < 0 || b->batch > 65535 || b->columns < 0 || b->max_q < 0 || b->max_kv < 0 ||
+      tokens < 0 || tokens > 0x7FFFFFFFll || b->table_ld < b->columns)
+    return FP4_ERR_SHAPE;
+  if ((int64_t)b->columns * c->page_size > 0x7FFFFFFFll) return FP4_ERR_SHAPE;
+  if (pointers && b->batch > 0) {
+    if (!b->kv_lens || !b->cu_q || (b->columns > 0 && !b->page_table)) return FP4_ERR_NULL;
+    if (!aligned(b->page_table, 4) || !aligned(b->kv_lens, 4) || !aligned(b->cu_q, 4))
+      return FP4_ERR_ALIGN;
+  }
+  return FP4_OK;
+}
+
+KvCacheArgs layer_of(const fp4_kv_cache* c, int32_t layer) {
+  KvCacheArgs a{};
+  const int64_t rows = layer * c->pages * c->heads * c->page_size;
+  const int64_t code = c->head_dim / 2, scale = c->head_dim / block_of(c);
+  a.k_codes = c->k_codes ? c->k_codes + rows * code : nullptr;
+  a.v_codes = c->v_codes ? c->v_codes + rows * code : nullptr;
+  a.k_scales = c->k_scales ? c->k_scales + rows * scale : nullptr;
+  a.v_scales = c->v_scales ? c->v_scales + rows * scale : nullptr;
+  a.k_scale = c->k_scale ? c->k_scale + layer : nullptr;
+  a.v_scale = c->v_scale ? c->v_scale + layer : nullptr;
+  a.pages = c->pages;
+  a.format = c->format;
+  a.heads = c->heads;
+  a.dim = c->head_dim;
+  a.page_log2 = log2_of(c->page_size);
+  a.rht = c->rht;
+  a.signs = c->rht ? fp4_rht_signs(c->rht_seed) : 0u;
+  return a;
+}
+
+KvBatchArgs batch_of(const fp4_kv_cache* c, const fp4_kv_batch* b, int64_t tokens) {
+  KvBatchArgs a{};
+  a.page_table = b->page_table;
+  a.table_ld = b->table_ld;
+  a.kv_lens = b->kv_lens;
+  a.cu_q = b->cu_q;
+  a.batch = b->batch;
+  a.columns = b->columns;
+  a.max_q = b->max_q < tokens ? b->max_q : (int)tokens;
+  const int cap = b->columns * c->page_size;
+  a.max_kv = b->max_kv > 0 && b->max_kv < cap ? b->max_kv : cap;
+  a.tokens = tokens;
+  return a;
+}
+
+KvPool pool_of(const fp4_kv_cache* c) {
+  KvPool p{};
+  p.k_codes = c->k_codes;
+  p.k_scales = c->k_scales;
+  p.v_codes = c->v_codes;
+  p.v_scales = c->v_scales;
+  p.pages = c->pages;
+  p.layers = c->layers;
+  p.heads = c->heads;
+  p.page_log2 = log2_of(c->page_size);
+  p.code_row = c->head_dim / 2;
+  p.scale_row = c->head_dim / block_of(c);
+  return p;
+}
+
+// Geometry, layer and batch: what append, gather and attention share.
+fp4_status check_call(const fp4_kv_cache* c, int32_t layer, const fp4_kv_batch* b,
+                      int64_t tokens) {
+  fp4_status st = check_geometry(c);
+  if (st != FP4_OK) return st;
+  if (layer < 0 || layer >= c->layers) return FP4_ERR_SHAPE;
+  if ((st = check_batch(c, b, tokens, true)) != FP4_OK) return st;
+  return check_arrays(c, true);
+}
+
+// Append and gather: one lane per block (16-element group); lanes of the
+// longest sequence in 31 bits.
+fp4_status check_units(const fp4_kv_cache* c, const KvBatchArgs& b, int32_t unit) {
+  return (int64_t)b.max_q * 2 * c->heads * (c->head_dim / unit) > 0x7FFFFFFFll ? FP4_ERR_SHAPE
+                                                                               : FP4_OK;
+}
+
+fp4_status check_attention(const fp4_kv_cache* c, const fp4_kv_batch* b, int32_t q_heads,
+                           int64_t tokens, int32_t window, int32_t sinks) {
+  if (q_heads < 1 || q_heads > 65536 || q_heads % c->heads || window < 0 || sinks < 0)
+    return FP4_ERR_SHAPE;
+  const KvBatchArgs k = batch_of(c, b, tokens);
+  if ((int64_t)k.max_q * q_heads > 0x3FFFFFFFll) return FP4_ERR_SHAPE;
+  const KvAttentionPlan p = fp4_plan_kv_attention(layer_of(c, 0), k, q_heads, window, sinks);
+  if ((int64_t)k.batch * c->heads * p.row_tiles * p.splits > 0x7FFFFFFFll) return FP4_ERR_SHAPE;
+  return FP4_OK;
+}
+
+fp4_status check_tables(const int32_t* table, int64_t table_ld, int64_t sequences,
+                        int32_t columns, const int32_t* refs) {
+  if (sequences < 0 || columns < 0 || table_ld < columns) return FP4_ERR_SHAPE;
+  if (!refs || (sequences > 0 && columns > 0 && !table)) return FP4_ERR_NULL;
+  return aligned(table, 4) && aligned(refs, 4) ? FP4_OK : FP4_ERR_ALIGN;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp4_status fp4_kv_append(const fp4_kv_cache* cache, int32_t layer, const fp4_kv_batch* batch,
+                         const void* k, int64_t k_token, int64_t k_head, const void* v,
+                         int64_t v_token, int64_t v_head, int32_t in_dtype, int64_t tokens,
+                         void* stream) {
+  fp4_status st = check_call(cache, layer, batch, tokens);
+  if (st != FP4_OK) return st;
+  if (in_dtype != FP4_BF16 && in_dtype != FP4_F32) return FP4_ERR_DTYPE;
+  KvAppendLaunch q{};
+  q.batch = batch_of(cache, batch, tokens);
+  if ((st = check_units(cache, q.batch, block_of(cache))) != FP4_OK) return st;
+  if (tokens == 0 || q.batch.batch == 0 || q.batch.max_q == 0 || q.batch.columns == 0)
+    return FP4_OK;
+  if (!k || !v) return FP4_ERR_NULL;
+  const int64_t size = in_dtype == FP4_BF16 ? 2 : 4;
+  if (!aligned(k, 16) || !aligned(v, 16) || !stride16(k_token, size) || !stride16(k_head, size) ||
+      !stride16(v_token, size) || !stride16(v_head, size))
+    return FP4_ERR_ALIGN;
+  q.cache = layer_of(cache, layer);
+  q.k = k;
+  q.v = v;
+  q.k_token = k_token;
+  q.k_head = k_head;
+  q.v_token = v_token;
+  q.v_head = v_head;
+  q.dtype = in_dtype;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return fp4_launch_status(fp4_launch_kv_append(q, s), s);
+}
+
+fp4_status fp4_kv_gather(const fp4_kv_cache* cache, int32_t layer, const fp4_kv_batch* batch,
+                         void* k_out, void* v_out, int64_t out_token, int64_t out_head,
+                         int32_t out_dtype, int64_t tokens, void* stream) {
+  fp4_status st = check_call(cache, layer, batch, tokens);
+  if (st != FP4_OK) return st;
+  if (out_dtype != FP4_BF16 && out_dtype != FP4_F32) return FP4_ERR_DTYPE;
+  KvGatherLaunch q{};
+  q.batch = batch_of(cache, batch, tokens);
+  if ((st = check_units(cache, q.batch, 16)) != FP4_OK) return st;
+  if (tokens == 0 || q.batch.batch == 0 || q.batch.max_q == 0) return FP4_OK;
+  if (!k_out || !v_out) return FP4_ERR_NULL;
+  const int64_t size = out_dtype == FP4_BF16 ? 2 : 4;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !stride16(out_token, size) ||
+      !stride16(out_head, size))
+    return FP4_ERR_ALIGN;
+  q.cache = layer_of(cache, layer);
+  q.k = k_out;
+  q.v = v_out;
+  q.token = out_token;
+  q.head = out_head;
+  q.dtype = out_dtype;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return fp4_launch_status(fp4_launch_kv_gather(q, s), s);
+}
+
+size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_batch* batch,
+                                        int32_t q_heads, int64_t tokens, int32_t window,
+                                        int32_t sinks) {
+  if (check_geometry(cache) != FP4_OK || check_batch(cache, batch, tokens, false) != FP4_OK ||
+      check_attention(cache, batch, q_heads, tokens, window, sinks) != FP4_OK)
+    return 0;
+  return fp4_plan_kv_attention(layer_of(cache, 0), batch_of(cache, batch, tokens), q_heads, window,
+                               sinks)
+      .bytes;
+}
+
+fp4_status fp4_kv_attention(const fp4_kv_cache* cache, int32_t layer, const fp4_kv_batch* batch,
+                            const void* q, int64_t q_token, int64_t q_head, int32_t q_heads,
+                            int64_t tokens, float scale, int32_t window, int32_t sinks, void* out,
+                            int32_t out_dtype, int64_t out_token, int64_t out_head, float* lse,
+                            void* workspace, size_t ws_bytes, void* stream) {
+  fp4_status st = check_call(cache, layer, batch, tokens);
+  if (st != FP4_OK) return st;
+  if (out_dtype != FP4_BF16 && out_dtype != FP4_F32) return FP4_ERR_DTYPE;
+  if (!(scale - scale == 0.0f)) return FP4_ERR_SHAPE;  // finite
+  if ((st = check_attention(cache, batch, q_heads, tokens, window, sinks)) != FP4_OK) return st;
+  KvAttentionLaunch a{};
+  a.batch = batch_of(cache, batch, tokens);
+  if (tokens == 0 || a.batch.batch == 0 || a.batch.max_q == 0) return FP4_OK;
+  if (!q || !out) return FP4_ERR_NULL;
+  const int64_t size = out_dtype == FP4_BF16 ? 2 : 4;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !stride16(q_token, 2) ||
+      !stride16(q_head, 2) || !stride16(out_token, size) || !stride16(out_head, size))
+    return FP4_ERR_ALIGN;
+  a.cache = layer_of(cache, layer);
+  const size_t need =
+      fp4_plan_kv_attention(a.cache, a.batch, q_heads, window, sinks).bytes;
+  if (need) {
+    if (!workspace || ws_bytes < need) return FP4_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return FP4_ERR_ALIGN;
+  }
+  a.q = q;
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.q_heads = q_heads;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.out_token = out_token;
+  a.out_head = out_head;
+  a.lse = lse;
+  a.workspace = workspace;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return fp4_launch_status(fp4_launch_kv_attention(a, s), s);
+}
+
+fp4_status fp4_kv_copy_pages(const fp4_kv_cache* cache, const int32_t* src, const int32_t* dst,
+                             const int32_t* tokens, int32_t n, void* stream) {
+  fp4_status st = check_geometry(cache);
+  if (st != FP4_OK) return st;
+  if (n < 0) return FP4_ERR_SHAPE;
+  if (n == 0) return FP4_OK;
+  if ((st = check_arrays(cache, false)) != FP4_OK) return st;
+  if (!src || !dst) return FP4_ERR_NULL;
+  if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(tokens, 4)) return FP4_ERR_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return fp4_launch_status(fp4_launch_kv_copy(pool_of(cache), src, dst, tokens, n, s), s);
+}
+
+fp4_status fp4_kv_fork(const fp4_kv_cache* cache, int32_t* page_table, int64_t table_ld,
+                       int64_t sequences, int32_t columns, int32_t* lens, int32_t* refs,
+                       const int32_t* parents, const int32_t* children, int32_t n,
+                       int32_t* failed, void* workspace, size_t ws_bytes, void* stream) {
+  fp4_status st = check_geometry(cache);
+  if (st != FP4_OK) return st;
+  if ((st = check_tables(page_table, table_ld, sequences, columns, refs)) != FP4_OK) return st;
+  if (n < 0 || (int64_t)columns * cache->page_size > 0x7FFFFFFFll) return FP4_ERR_SHAPE;
+  if (!failed) return FP4_ERR_NULL;
+  if (!aligned(failed, 4)) return FP4_ERR_ALIGN;
+  if (n > 0) {
+    if ((st = check_arrays(cache, false)) != FP4_OK) return st;
+    if (!lens || !parents || !children) return FP4_ERR_NULL;
+    if (!aligned(lens, 4) || !aligned(parents, 4) || !aligned(children, 4)) return FP4_ERR_ALIGN;
+    if (!workspace || ws_bytes < 16 * (size_t)n) return FP4_ERR_WORKSPACE;
+    if (!aligned(workspace, 4)) return FP4_ERR_ALIGN;
+  }
+  const KvTables t{page_table, table_ld, sequences, columns, lens, refs};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return fp4_launch_status(fp4_launch_kv_fork(pool_of(cache), t, parents, children, n, failed,
+                                              static_cast<int32_t*>(workspace), s),
+                           s);
+}
+
+fp4_status fp4_kv_free(int32_t* page_table, int64_t table_ld, int64_t sequences, int32_t columns,
+                       int32_t* lens, int32_t* refs, int64_t pages, int32_t page_size,
+                       const int32_t* seqs, int32_t n, int32_t window, int32_t sinks,
+                       void* stream) {
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return FP4_ERR_SHAPE;
+  if (pages < 1 || pages > 0x7FFFFFFFll || n < 0 || window < 0 || sinks < 0) return FP4_ERR_SHAPE;
+  fp4_status st = check_tables(page_table, table_ld, sequences, columns, refs);
+  if (st != FP4_OK) return st;
+  if ((int64_t)columns * page_size > 0x7FFFFFFFll) return FP4_ERR_SHAPE;
+  if (n == 0 || sequences == 0) return FP4_OK;
+  if (!lens || !seqs) return FP4_ERR_NULL;
+  if (!aligned(lens, 4) || !aligned(seqs, 4)) return FP4_ERR_ALIGN;
+  const KvTables t{page_table, table_ld, sequences, columns, lens, refs};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return fp4_launch_status(
+      fp4_launch_kv_free(t, pages, log2_of(page_size), seqs, n, window, sinks, s), s);
+}
+
+fp4_status fp4_kv_compact(const fp4_kv_cache* cache, int32_t* page_table, int64_t table_ld,
+                          int64_t sequences, int32_t columns, int32_t* refs, int32_t* place,
+                          int32_t* used, void* workspace, size_t ws_bytes, void* stream) {
+  fp4_status st = check_geometry(cache);
+  if (st != FP4_OK) return st;
+  if ((st = check_tables(page_table, table_ld, sequences, columns, refs)) != FP4_OK) return st;
+  if ((st = check_arrays(cache, false)) != FP4_OK) return st;
+  if (!place || !used) return FP4_ERR_NULL;
+  if (!aligned(place, 4) || !aligned(used, 4)) return FP4_ERR_ALIGN;
+  if (!workspace || ws_bytes < 4 * ((size_t)cache->pages + 3)) return FP4_ERR_WORKSPACE;
+  if (!aligned(workspace, 4)) return FP4_ERR_ALIGN;
+  const KvTables t{page_table, table_ld, sequences, columns, nullptr, refs};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return fp4_launch_status(fp4_launch_kv_compact(pool_of(cache), t, place, used,
+                                                 static_cast<int32_t*>(workspace), s),
+                           s);
+}
+
+}  // extern "C"

@@ -1,0 +1,421 @@
+// fp4_kv_pages.hip -- pages of a 4-bit cache: copied, forked, given back and
+// packed, for all layers in one call.
+//
+// The tables live on the device: page_table [sequences][columns] (page ids,
+// -1: none), lens [sequences], refs [pages] (rows that hold the page; 0:
+// free).  Nothing is read back by the host, so the calls can sit in a
+// captured graph.  A call that has to choose pages does it in one workgroup
+// (the ids in order, each thread a contiguous run of them, one scan over the
+// threads), which writes a list of moves; a second launch moves the pages
+// and rewrites the tables.  The result does not depend on timing: free pages
+// are taken lowest id first, in the order of the caller's list, and counts
+// change by integer atomics.
+//
+// Bound by the bytes moved, each read and written once: a page of one layer
+// is heads * page * (D + 2 * D / B) bytes, copied 16 bytes to a lane.
+#include "fp4_kv_pages.h"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kListThreads = 1024;
+
+// ------------------------------------------------------------ moving pages
+// One array of the cache: `row` bytes of a token and head.
+struct Array {
+  uint8_t* base;
+  int row;
+};
+
+// The first `tokens` tokens of every head of a page.  A head's tokens are
+// contiguous; pages hold multiples of 16 tokens, so every head starts on a
+// multiple of 32 bytes, and rows have an even number of bytes.
+__device__ __forceinline__ void copy_page(const Array& x, int64_t layer_pages, int heads, int page,
+                                          int64_t src, int64_t dst, int tokens) {
+  const int64_t pitch = (int64_t)page * x.row;  // bytes of one head
+  const uint8_t* from = x.base + (layer_pages + src) * heads * pitch;
+  uint8_t* to = x.base + (layer_pages + dst) * heads * pitch;
+  if (tokens == page) {  // the whole page is one run
+    const int n = (int)(heads * pitch / 16);
+    const uint4* x4 = reinterpret_cast<const uint4*>(from);
+    uint4* y4 = reinterpret_cast<uint4*>(to);
+    int i = threadIdx.x;
+    for (; i + 7 * kThreads < n; i += 8 * kThreads) {  // eight loads in flight
+      uint4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = x4[i + k * kThreads];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y4[i + k * kThreads] = v[k];
+    }
+    for (; i < n; i += kThreads) y4[i] = x4[i];
+    return;
+  }
+  const int bytes = tokens * x.row, n = bytes / 16;
+  const int total = heads * n;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < total; i += kThreads) {
+    const int h = i / n;
+    const int64_t at = h * pitch + (int64_t)(i - h * n) * 16;
+    *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(from + at);
+  }
+  const int rest = (bytes - n * 16) / 2;  // 2-byte pieces of a head's end
+  for (int i = threadIdx.x; i < heads * rest; i += kThreads) {
+    const int h = i / rest;
+    const int64_t at = h * pitch + n * 16 + (i - h * rest) * 2;
+    *reinterpret_cast<uint16_t*>(to + at) = *reinterpret_cast<const uint16_t*>(from + at);
+  }
+}
+
+struct MoveArgs {
+  KvPool pool;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* tokens;  // null: whole pages
+  const int32_t* count;   // null: n
+  int n;
+  // bookkeeping beside the moves
+  int32_t* table;
+  int64_t table_ld;
+  int columns;
+  int64_t sequences;
+  int32_t* lens;
+  int32_t* refs;
+  const int32_t* parents;
+  const int32_t* children;
+  const int32_t* place;
+  int table_groups;  // workgroups that keep the tables, ahead of the movers
+};
+
+enum : int { kCopy, kFork, kCompact };
+
+// Row of a fork: the parent's shared pages, then the copied page.  dst: the
+// copied page, -1 for none, -2 where no page was free (the child stays empty).
+__device__ void fork_row(const MoveArgs& a, int i) {
+  const int parent = a.parents[i], child = a.children[i];
+  if (child < 0 || child >= a.sequences) return;
+  const bool has = parent >= 0 && parent < a.sequences && a.dst[i] != -2;
+  const int64_t cap = (int64_t)a.columns << a.pool.page_log2;
+  int len = has ? a.lens[parent] : 0;
+  len = len < 0 ? 0 : (len > cap ? (int)cap : len);
+  const int full = len >> a.pool.page_log2;
+  for (int c = threadIdx.x; c < a.columns; c += kThreads) {
+    int page = -1;
+    if (c < full) {
+      page = a.table[parent * a.table_ld + c];
+      if (page >= 0 && page < a.pool.pages) atomicAdd(a.refs + page, 1);
+      else page = -1;
+    } else if (has && c == full && a.dst[i] >= 0) {
+      page = a.dst[i];
+      a.refs[page] = 1;
+    }
+    a.table[child * a.table_ld + c] = page;
+  }
+  if (threadIdx.x == 0) a.lens[child] = len;
+}
+
+template <int MODE>
+__global__ __launch_bounds__(kThreads) void kv_move_kernel(MoveArgs a) {
+  if constexpr (MODE == kFork) {
+    for (int i = blockIdx.x; i < a.n && (int)blockIdx.x < a.table_groups; i += a.table_groups)
+      fork_row(a, i);
+  } else if constexpr (MODE == kCompact) {
+    if ((int)blockIdx.x < a.table_groups) {
+      const int64_t total = a.sequences * a.columns;
+      for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
+           i += (int64_t)a.table_groups * kThreads) {
+        const int64_t r = i / a.columns;
+        int32_t* p = a.table + r * a.table_ld + (i - r * a.columns);
+        const int page = *p;
+        *p = page >= 0 && page < a.pool.pages ? a.place[page] : -1;
+      }
+    }
+  }
+  if ((int)blockIdx.x < a.table_groups) return;
+  // an item: a move, one layer, K or V
+  const int n = a.count ? *a.count : a.n;
+  const int64_t per = 2ll * a.pool.layers, items = n * per;
+  const int page = 1 << a.pool.page_log2;
+  for (int64_t it = blockIdx.x - a.table_groups; it < items; it += gridDim.x - a.table_groups) {
+    const int64_t i = it / per;
+    const int part = (int)(it - i * per), layer = part >> 1;
+    const int src = a.src[i], dst = a.dst[i];
+    if (src < 0 || src >= a.pool.pages || dst < 0 || dst >= a.pool.pages || src == dst) continue;
+    int tokens = a.tokens ? a.tokens[i] : page;
+    tokens = tokens < 0 ? 0 : (tokens > page ? page : tokens);
+    if (tokens == 0) continue;
+    const int64_t first = (int64_t)layer * a.pool.pages;
+    const bool v = part & 1;
+    copy_page({v ? a.pool.v_codes : a.pool.k_codes, a.pool.code_row}, first, a.pool.heads, page, src,
+              dst, tokens);
+    copy_page({v ? a.pool.v_scales : a.pool.k_scales, a.pool.scale_row}, first, a.pool.heads, page,
+              src, dst, tokens);
+  }
+}
+
+// ------------------------------------------------------------------- lists
+// Sum over the threads before this one, and over all.
+__device__ __forceinline__ int scan(int v, int& all) {
+  __shared__ int sums[kListThreads / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // the sums of the scan before were read
+  if (lane == 63) sums[wave] = x;
+  __syncthreads();
+  int before = 0;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kListThreads / 64; ++w) {
+    if (w < wave) before += sums[w];
+    all += sums[w];
+  }
+  return before + x - v;
+}
+
+// This thread's run of n items.
+struct Run {
+  int64_t begin, end;
+  __device__ __forceinline__ explicit Run(int64_t n) {
+    const int64_t per = (n + kListThreads - 1) / kListThreads;
+    begin = threadIdx.x * per < n ? threadIdx.x * per : n;
+    end = begin + per < n ? begin + per : n;
+  }
+};
+
+struct ForkArgs {
+  const int32_t* table;
+  int64_t table_ld, sequences;
+  int columns, page_log2;
+  const int32_t* lens;
+  const int32_t* refs;
+  int64_t pages;
+  const int32_t* parents;
+  int n;
+  int32_t* src;
+  int32_t* dst;
+  int32_t* tokens;
+  int32_t* found;  // the lowest free pages, as many as are needed
+  int32_t* failed;
+};
+
+// Page that fork i has to copy (its parent's last, partly filled one) and
+// its tokens; -1 where there is none.
+__device__ __forceinline__ int fork_source(const ForkArgs& a, int64_t i, int& tokens) {
+  tokens = 0;
+  const int parent = a.parents[i];
+  if (parent < 0 || parent >= a.sequences) return -1;
+  const int64_t cap = (int64_t)a.columns << a.page_log2;
+  const int len = a.lens[parent];
+  if (len <= 0 || len >= cap) return -1;
+  const int rem = len & ((1 << a.page_log2) - 1);
+  if (rem == 0) return -1;
+  const int page = a.table[parent * a.table_ld + (len >> a.page_log2)];
+  if (page < 0 || page >= a.pages) return -1;
+  tokens = rem;
+  return page;
+}
+
+__global__ __launch_bounds__(kListThreads) void kv_fork_list_kernel(ForkArgs a) {
+  // which forks copy a page, and which of the free pages each takes
+  const Run f(a.n);
+  int mine = 0, need, free_pages;
+  for (int64_t i = f.begin; i < f.end; ++i) {
+    int tokens;
+    const int src = fork_source(a, i, tokens);
+    a.src[i] = src;
+    a.tokens[i] = tokens;
+    mine += src >= 0;
+  }
+  int rank = scan(mine, need);
+  const Run p(a.pages);
+  int zeros = 0;
+  for (int64_t i = p.begin; i < p.end; ++i) zeros += a.refs[i] == 0;
+  int at = scan(zeros, free_pages);
+  for (int64_t i = p.begin; i < p.end && at < need; ++i)
+    if (a.refs[i] == 0) a.found[at++] = (int32_t)i;
+  __syncthreads();
+  for (int64_t i = f.begin; i < f.end; ++i) {
+    int dst = -1;
+    if (a.src[i] >= 0) {
+      dst = rank < free_pages ? a.found[rank] : -2;
+      ++rank;
+    }
+    a.dst[i] = dst;
+  }
+  if (threadIdx.x == 0) *a.failed = need > free_pages ? need - free_pages : 0;
+}
+
+struct CompactArgs {
+  int32_t* refs;
+  int64_t pages;
+  int32_t* place;  // new id of each page, -1 for a free one
+  int32_t* used;
+  int32_t* src;  // moves
+  int32_t* dst;
+  int32_t* moves;
+};
+
+// Pages in use with ids past their number n go to the free ids below n, in
+// order: as few moves as there can be, and no page is both read and written.
+__global__ __launch_bounds__(kListThreads) void kv_compact_list_kernel(CompactArgs a) {
+  const Run p(a.pages);
+  int mine = 0, n;
+  for (int64_t i = p.begin; i < p.end; ++i) mine += a.refs[i] > 0;
+  scan(mine, n);
+  int movers = 0, holes = 0, all_movers, all_holes;
+  for (int64_t i = p.begin; i < p.end; ++i) {
+    const bool in_use = a.refs[i] > 0;
+    movers += in_use && i >= n;
+    holes += !in_use && i < n;
+  }
+  int mover = scan(movers, all_movers), hole = scan(holes, all_holes);
+  for (int64_t i = p.begin; i < p.end; ++i) {
+    const bool in_use = a.refs[i] > 0;
+    if (in_use && i >= n) a.src[mover++] = (int32_t)i;
+    if (!in_use && i < n) a.dst[hole++] = (int32_t)i;
+    a.place[i] = in_use ? (int32_t)i : -1;
+  }
+  __syncthreads();  // every hole has its mover: both number n minus the used ids below n
+  for (int k = threadIdx.x; k < all_movers; k += kListThreads) {
+    const int from = a.src[k], to = a.dst[k];
+    a.place[from] = to;
+    a.refs[to] = a.refs[from];
+    a.refs[from] = 0;
+  }
+  if (threadIdx.x == 0) {
+    *a.used = n;
+    *a.moves = all_movers;
+  }
+}
+
+// -------------------------------------------------------------- giving back
+struct FreeArgs {
+  int32_t* table;
+  int64_t table_ld, sequences;
+  int columns, page_log2;
+  int32_t* lens;
+  int32_t* refs;
+  int64_t pages;
+  const int32_t* seqs;
+  int n, window, sinks;
+};
+
+// A workgroup per listed sequence.  Without a window the whole row goes;
+// under one, the pages that hold neither one of the first `sinks` tokens nor
+// one of the last `window`.
+__global__ __launch_bounds__(kThreads) void kv_free_kernel(FreeArgs a) {
+  const int seq = a.seqs[blockIdx.x];
+  if (seq < 0 || seq >= a.sequences) return;
+  int32_t* row = a.table + seq * a.table_ld;
+  const int64_t keep = (int64_t)a.lens[seq] - a.window;
+  __syncthreads();  // the length is read before it is cleared
+  for (int c = threadIdx.x; c < a.columns; c += kThreads) {
+    const int page = row[c];
+    if (page == -1) continue;
+    const int64_t t = (int64_t)c << a.page_log2;
+    if (a.window > 0 && (t < a.sinks || t + (1 << a.page_log2) > keep)) continue;
+    if (page >= 0 && page < a.pages) atomicSub(a.refs + page, 1);
+    row[c] = -1;
+  }
+  if (a.window == 0 && threadIdx.x == 0) a.lens[seq] = 0;
+}
+
+// Workgroups that move pages: enough to fill the chip, no more than there
+// are items.
+unsigned mover_groups(int64_t items) {
+  const int64_t most = 256 * 8;
+  return (unsigned)(items < 1 ? 1 : (items < most ? items : most));
+}
+
+}  // namespace
+
+hipError_t fp4_launch_kv_copy(const KvPool& pool, const int32_t* src, const int32_t* dst,
+                              const int32_t* tokens, int n, hipStream_t s) {
+  MoveArgs a{};
+  a.pool = pool;
+  a.src = src;
+  a.dst = dst;
+  a.tokens = tokens;
+  a.n = n;
+  kv_move_kernel<kCopy><<<mover_groups((int64_t)n * 2 * pool.layers), kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t fp4_launch_kv_fork(const KvPool& pool, const KvTables& t, const int32_t* parents,
+                              const int32_t* children, int n, int32_t* failed, int32_t* ws,
+                              hipStream_t s) {
+  ForkArgs f{};
+  f.table = t.table;
+  f.table_ld = t.table_ld;
+  f.sequences = t.sequences;
+  f.columns = t.columns;
+  f.page_log2 = pool.page_log2;
+  f.lens = t.lens;
+  f.refs = t.refs;
+  f.pages = pool.pages;
+  f.parents = parents;
+  f.n = n;
+  f.src = ws;
+  f.dst = ws + n;
+  f.tokens = ws + 2 * (int64_t)n;
+  f.found = ws + 3 * (int64_t)n;
+  f.failed = failed;
+  kv_fork_list_kernel<<<1, kListThreads, 0, s>>>(f);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || n == 0) return e;
+  MoveArgs a{};
+  a.pool = pool;
+  a.src = f.src;
+  a.dst = f.dst;
+  a.tokens = f.tokens;
+  a.n = n;
+  a.table = t.table;
+  a.table_ld = t.table_ld;
+  a.columns = t.columns;
+  a.sequences = t.sequences;
+  a.lens = t.lens;
+  a.refs = t.refs;
+  a.parents = parents;
+  a.children = children;
+  a.table_groups = n < 256 ? n : 256;
+  kv_move_kernel<kFork>
+      <<<a.table_groups + mover_groups((int64_t)n * 2 * pool.layers), kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t fp4_launch_kv_free(const KvTables& t, int64_t pages, int page_log2, const int32_t* seqs,
+                              int n, int window, int sinks, hipStream_t s) {
+  FreeArgs a{t.table, t.table_ld, t.sequences, t.columns, page_log2, t.lens, t.refs,
+             pages,   seqs,       n,           window,    sinks};
+  kv_free_kernel<<<n, kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t fp4_launch_kv_compact(const KvPool& pool, const KvTables& t, int32_t* place,
+                                 int32_t* used, int32_t* ws, hipStream_t s) {
+  // at most as many moves as half the pages: a mover and a hole each
+  const int64_t half = pool.pages / 2 + 1;
+  CompactArgs c{t.refs, pool.pages, place, used, ws + 1, ws + 1 + half, ws};
+  kv_compact_list_kernel<<<1, kListThreads, 0, s>>>(c);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  MoveArgs a{};
+  a.pool = pool;
+  a.src = c.src;
+  a.dst = c.dst;
+  a.count = c.moves;
+  a.table = t.table;
+  a.table_ld = t.table_ld;
+  a.columns = t.columns;
+  a.sequences = t.sequences;
+  a.place = place;
+  const int64_t entries = t.sequences * t.columns;
+  a.table_groups = (int)(entries < 256 * kThreads ? (entries + kThreads - 1) / kThreads : 256);
+  kv_move_kernel<kCompact>
+      <<<a.table_groups + mover_groups(half * 2 * pool.layers), kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}

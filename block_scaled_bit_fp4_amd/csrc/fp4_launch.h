@@ -102,3 +102,5 @@ hipError_t fp4_launch_dequantize(const DequantLaunch& q, hipStream_t s);
 hipError_t fp4_launch_rht(const RhtLaunch& q, hipStream_t s);
 hipError_t fp4_launch_gemm_mx(const GemmLaunch& q, hipStream_t s);
 hipError_t fp4_launch_write_scalar(float* p, float v, hipStream_t s);
+// The status of a finished launch (FP4_DEBUG_SYNC=1: after a synchronization).
+int32_t fp4_launch_status(hipError_t e, hipStream_t s);

@@ -311,6 +311,146 @@ fp4_status fp4_gemm_mx(const uint8_t* a_codes, const uint8_t* a_scales,
                        const uint8_t* b_codes, const uint8_t* b_scales, int64_t M, int64_t N,
                        int64_t K, void* c, int32_t c_dtype, int64_t ldc, void* stream);
 
+/* ------------------------------------------------------- 4-bit KV cache
+ *
+ * A cache of keys and values in pages, held in a block-scaled FP4 format,
+ * the attention that reads it, and the moves of its pages.
+ *
+ * Layout: k_codes, v_codes [layers][pages][heads][page_size][head_dim / 2]
+ * bytes (element 2j in the low nibble of byte j) and k_scales, v_scales
+ * [layers][pages][heads][page_size][head_dim / B] bytes, all dense.  Formats
+ * FP4_NVFP4 (B = 16, E4M3 scales, and the tensor scale of fp4_quantize's
+ * FP4_TS_GIVEN mode, one float per layer for K and one for V), FP4_MXFP4
+ * and FP4_MXFP4_OAS (B = 32, E8M0).  With rht = 1 every row is rotated by
+ * the 16-point RHT of rht_seed along head_dim before it is quantized;
+ * attention rotates q alike and rotates its output back, and reading rows
+ * back undoes it.  heads is the number of key / value heads.
+ *
+ * A batch names the tokens of a call.  Sequence b has kv_lens[b] tokens in
+ * the cache, the new ones of this call included; token t of it lies at
+ * offset t % page_size of page page_table[b * table_ld + t / page_size].
+ * Its new tokens are rows cu_q[b] .. cu_q[b + 1] - 1 of the tensors of the
+ * call and stand at its last positions: row cu_q[b] + i at position
+ * kv_lens[b] - (cu_q[b + 1] - cu_q[b]) + i.  max_q is at least the longest
+ * count of new tokens (rows past it are left out), max_kv at least the
+ * longest length (it only sizes the split of the work; 0 takes columns *
+ * page_size).  page_table, kv_lens and cu_q are device memory; their
+ * values are not checked on the host, and no value makes a kernel read or
+ * write outside the arrays: lengths past columns * page_size are cut there,
+ * and a page id outside [0, pages) (-1 by convention) means no page: its
+ * tokens are not written, read back as zeros and are not attended to. */
+typedef struct {
+  int32_t format;    /* FP4_NVFP4 / FP4_MXFP4 / FP4_MXFP4_OAS */
+  int32_t layers;
+  int32_t heads;     /* key / value heads, 1 .. 1024 */
+  int32_t head_dim;  /* 64, 128 or 256 */
+  int32_t page_size; /* 16, 32, 64, 128 or 256 tokens */
+  int32_t rht;       /* 0 / 1 */
+  uint64_t rht_seed;
+  int64_t pages;     /* 1 .. 2^31 - 1 */
+  uint8_t* k_codes;  /* arrays 16-byte aligned */
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* k_scale; /* NVFP4: [layers] finite factors, device memory; else unused */
+  const float* v_scale;
+} fp4_kv_cache;
+
+typedef struct {
+  const int32_t* page_table; /* [batch][table_ld], columns used */
+  int64_t table_ld;
+  const int32_t* kv_lens; /* [batch] */
+  const int32_t* cu_q;    /* [batch + 1] */
+  int32_t batch;          /* 0 .. 65535 */
+  int32_t columns;        /* columns * page_size < 2^31 */
+  int32_t max_q;
+  int32_t max_kv;
+} fp4_kv_batch;
+
+/* Quantize the new tokens' keys and values (k, v: tokens x heads x head_dim,
+ * BF16 or FP32, strides in elements, the last dimension dense) into their
+ * places in layer `layer`: the codes and scales of fp4_quantize on the row
+ * axis, round to nearest even, with the layer's factor as the given tensor
+ * scale.  One launch, no workspace.  k, v 16-byte aligned, strides
+ * multiples of 16 bytes.  Two tokens with one place race. */
+fp4_status fp4_kv_append(const fp4_kv_cache* cache, int32_t layer, const fp4_kv_batch* batch,
+                         const void* k, int64_t k_token, int64_t k_head, const void* v,
+                         int64_t v_token, int64_t v_head, int32_t in_dtype, int64_t tokens,
+                         void* stream);
+
+/* The inverse: the keys and values that the batch's new tokens have in the
+ * cache, as fp4_dequantize gives them (inverse RHT included), into k_out and
+ * v_out (tokens x heads x head_dim, FP32 or BF16, same strides for both).
+ * With all of a sequence's tokens as its new ones this reads it whole. */
+fp4_status fp4_kv_gather(const fp4_kv_cache* cache, int32_t layer, const fp4_kv_batch* batch,
+                         void* k_out, void* v_out, int64_t out_token, int64_t out_head,
+                         int32_t out_dtype, int64_t tokens, void* stream);
+
+/* Bytes of device workspace that fp4_kv_attention needs (0 when the keys
+ * are not split); contents need no initialization.  0 too for arguments
+ * that fp4_kv_attention refuses. */
+size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_batch* batch,
+                                        int32_t q_heads, int64_t tokens, int32_t window,
+                                        int32_t sinks);
+
+/* Causal attention of the batch's new tokens over the cache (their own keys
+ * and values included: append first).  q: tokens x q_heads x head_dim BF16,
+ * q_heads a multiple of heads; query head h reads key head h / (q_heads /
+ * heads).  A token at position p sees positions j <= p; with window > 0 only
+ * j > p - window, and the first `sinks` positions.  out (same shape, BF16
+ * or FP32) = softmax(scale * q K^T) V, 0 where nothing is visible; lse (NULL
+ * or tokens x q_heads floats, dense) the natural logarithm of the sum of
+ * exponentials, -inf there.  Rows that belong to no sequence are not
+ * written.  Scores, maxima, sums and outputs accumulate in binary32; q and
+ * the probabilities enter the matrix instructions in 16 bits (FP16 for
+ * NVFP4, BF16 for the MX formats).  K and V dequantize exactly.  Scores must
+ * be finite.  q and out 16-byte aligned, strides multiples of 16 bytes. */
+fp4_status fp4_kv_attention(const fp4_kv_cache* cache, int32_t layer, const fp4_kv_batch* batch,
+                            const void* q, int64_t q_token, int64_t q_head, int32_t q_heads,
+                            int64_t tokens, float scale, int32_t window, int32_t sinks, void* out,
+                            int32_t out_dtype, int64_t out_token, int64_t out_head, float* lse,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* Page moves, all layers at once (the factors are not touched).
+ *
+ * Tables: page_table [sequences][table_ld], columns used, -1 for no page;
+ * lens [sequences]; refs [pages], the number of rows that hold a page (0:
+ * free).  Ids and sequence numbers out of range are skipped, never
+ * dereferenced. */
+
+/* Page dst[i] takes the first tokens[i] tokens (NULL: all) of page src[i],
+ * i < n.  Pages of dst are distinct and none of src. */
+fp4_status fp4_kv_copy_pages(const fp4_kv_cache* cache, const int32_t* src, const int32_t* dst,
+                             const int32_t* tokens, int32_t n, void* stream);
+
+/* Sequence children[i] becomes a copy of parents[i], i < n: full pages are
+ * shared (refs + 1), a partly filled last page is copied into a free page,
+ * lowest id first in the order of the list.  *failed takes the number of
+ * forks that found no free page; their children are empty (length 0, no
+ * pages).  Children are distinct, hold no pages, and are no parents.
+ * workspace: 16 * n bytes, 4-byte aligned. */
+fp4_status fp4_kv_fork(const fp4_kv_cache* cache, int32_t* page_table, int64_t table_ld,
+                       int64_t sequences, int32_t columns, int32_t* lens, int32_t* refs,
+                       const int32_t* parents, const int32_t* children, int32_t n,
+                       int32_t* failed, void* workspace, size_t ws_bytes, void* stream);
+
+/* Give pages of the listed (distinct) sequences back: refs - 1, entry -1.
+ * window = 0: all of them, and the length becomes 0.  window > 0: those
+ * that hold none of the last `window` tokens and none of the first `sinks`;
+ * lengths stay. */
+fp4_status fp4_kv_free(int32_t* page_table, int64_t table_ld, int64_t sequences, int32_t columns,
+                       int32_t* lens, int32_t* refs, int64_t pages, int32_t page_size,
+                       const int32_t* seqs, int32_t n, int32_t window, int32_t sinks,
+                       void* stream);
+
+/* Pack the pages in use (refs > 0) into ids 0 .. *used - 1: those with ids
+ * past *used move to the free ids below it, in order.  Rewrites page_table
+ * and refs; place [pages] takes each page's new id (-1: it was free).
+ * workspace: 4 * (pages + 3) bytes, 4-byte aligned. */
+fp4_status fp4_kv_compact(const fp4_kv_cache* cache, int32_t* page_table, int64_t table_ld,
+                          int64_t sequences, int32_t columns, int32_t* refs, int32_t* place,
+                          int32_t* used, void* workspace, size_t ws_bytes, void* stream);
+
 /* The RHT sign mask of a seed (host function): low 16 bits of word 0 of
  * Philox4x32-10(key = seed, counter = (0, 0, 1, 0)); bit j set: d_j = -1. */
 uint16_t fp4_rht_signs(uint64_t rht_seed);
