@@ -74,8 +74,9 @@ struct KvAttentionPlan {
   bool prompt;    // the kernel for many rows
   int rows;       // rows of a workgroup
   int row_tiles;  // of the longest sequence
-  int splits;
-  size_t bytes;   // workspace
+  int splits;      // many rows: pieces of the keys
+  int64_t groups;  // workgroups
+  size_t bytes;    // workspace
 };
 
 KvAttentionPlan fp4_plan_kv_attention(const KvCacheArgs& c, const KvBatchArgs& b, int q_heads,

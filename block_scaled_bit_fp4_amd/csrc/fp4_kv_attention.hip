@@ -139,21 +139,25 @@ struct Args {
   int out_f32;
   int64_t out_token, out_head;
   float* lse;
-  // pieces of the keys: partial outputs [split][token][head][D], and (m, l)
-  // of each [split][token][head]
+  int row_tiles;
+  // Partial results.  Many rows: [split][token][head][D] and (m, l) of each.
+  // Few rows: slots of 16 * NT rows (Work, below), and where the work of each
+  // row tile of each sequence starts in the list.
   float* part;
   float2* part_ml;
-  int splits, row_tiles;
+  uint32_t* starts;
+  int splits, groups;
+  int join_rows;  // rows of a row tile that the longest sequence fills
 };
 
-// The keys that the rows of a workgroup see: the tiles of T keys that hold
-// the first `sinks` tokens, then those from the first row's window to the
-// last row's position, cut to this split.
+// The keys that rows i0 .. i1 (new tokens of a sequence) see, in tiles of T:
+// the tiles that hold the first `sinks` tokens, then those from the first
+// row's window to the last row's position.  n: how many.
 template <int T>
 struct Keys {
-  int sink_tiles, start, begin, end;  // tiles [begin, end) of the list
-  int lo, hi;                         // visible to some row: [lo, hi), and the sinks
-  __device__ __forceinline__ void init(const Args& a, const KvSeq& s, int i0, int i1, int split) {
+  int sink_tiles, start, n;
+  int lo, hi;  // visible to some row: [lo, hi), and the sinks
+  __device__ __forceinline__ void init(const Args& a, const KvSeq& s, int i0, int i1) {
     const int64_t p0 = s.pos + i0, p1 = s.pos + i1;
     const int64_t h = p1 + 1 < s.kv ? p1 + 1 : s.kv;
     hi = h < 0 ? 0 : (int)h;
@@ -163,35 +167,27 @@ struct Keys {
     sink_tiles = (sk + T - 1) / T;
     start = lo / T > sink_tiles ? lo / T : sink_tiles;
     const int last = (hi + T - 1) / T;
-    const int n = sink_tiles + (last > start ? last - start : 0);
-    // every split takes the same number of tiles whatever the sequence, so
-    // that lengths apart leave workgroups of equal work (the host sizes the
-    // splits by the longest list); a list past that bound is shared evenly
-    const int bound = (max_keys(a, s) + T - 1) / T + 2;
-    const int per = ((n > bound ? n : bound) + a.splits - 1) / a.splits;
-    const int64_t b = (int64_t)split * per;
-    begin = b < n ? (int)b : n;
-    end = b + per < n ? (int)(b + per) : n;
-  }
-  // Most keys a row tile of this call sees, by what the host knows.
-  static __device__ __forceinline__ int max_keys(const Args& a, const KvSeq& s) {
-    int64_t n = a.b.max_kv;
-    if (a.window > 0) {
-      const int64_t w = (int64_t)a.window + a.sinks + a.b.max_q;
-      if (w < n) n = w;
-    }
-    return (int)n;
+    n = sink_tiles + (last > start ? last - start : 0);
   }
   __device__ __forceinline__ int base(int u) const {
     return (u < sink_tiles ? u : start + u - sink_tiles) * T;
   }
 };
 
+// Most keys that a row tile of a call sees, by what the host knows.
+__host__ __device__ __forceinline__ int64_t max_keys(int64_t max_kv, int window, int sinks, int max_q) {
+  const int64_t w = (int64_t)window + sinks + max_q;
+  return window > 0 && w < max_kv ? w : max_kv;
+}
+
 // Page of the sixteen tokens from t on (t a multiple of 16, wave-uniform),
-// -1 if the sequence has none there.
+// -1 if the sequence has none there.  The table is read through the constant
+// address space: a scalar load, which does not wait in line behind the vector
+// loads of the tiles in flight.
 __device__ __forceinline__ int page_of(const Args& a, int seq, int t, int hi) {
   if (t >= hi) return -1;
-  const int p = a.b.page_table[seq * a.b.table_ld + (t >> a.c.page_log2)];
+  typedef const __attribute__((address_space(4))) int32_t* table_t;
+  const int p = ((table_t)a.b.page_table)[seq * a.b.table_ld + (t >> a.c.page_log2)];
   return p >= 0 && p < a.c.pages ? p : -1;
 }
 
@@ -276,17 +272,41 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // ============================================================ few new tokens
 // Rows (a new token and a query head of this key head) 16 * NT to a
 // workgroup of four waves.  Each wave takes every fourth tile of 32 keys of
-// the split on its own: K's codes go from global memory through registers
-// into the matrix instruction (a lane holds D / 4 codes of one token), V's
-// through the wave's own LDS.  No barrier until the four waves' results are
-// joined.
-constexpr int kFewThreads = 256, kFewWaves = 4, kFewKeys = 32;
+// the workgroup's piece on its own: K's codes go from global memory through
+// registers into the matrix instruction (a lane holds a quarter of a token's
+// row), V's through the wave's own LDS.  The rows of q, which all waves
+// multiply by, are rounded once by the workgroup and read from LDS.  No
+// barrier between that and the joining of the four waves' results.
+//
+// Bound by the cache's bytes; what it takes is bytes in flight.  A wave
+// keeps the next R - 1 tiles on their way in registers (no depth or
+// occupancy beyond that changed the time), and the workgroups' equal runs
+// keep every compute unit reading to the end.
+constexpr int kFewThreads = 256, kFewWaves = 4, kFewKeys = 32, kFewLeast = 4;
+
+// Tiles of a wave at work or on their way.
+__host__ __device__ constexpr int few_ring(int dim) { return dim == 64 ? 3 : 2; }
+
+// Workgroups of a compute unit at once (registers and LDS set it).
+__host__ __device__ constexpr int few_residents(int dim, int rows) {
+  return rows == 16 && dim <= 128 ? 3 : 2;
+}
+
+// A row of D columns is worked on in parts of C: in part p a lane of segment
+// g (of four) holds columns p * C + g * C / 4 and the C / 4 - 1 after it.
+template <int D>
+struct Few {
+  static constexpr int C = D < 128 ? D : 128, P = D / C;
+  static constexpr int W = C / 32;        // words of codes per lane and part = QK instructions
+  static constexpr int J = C / 16;        // PV instructions (16 columns) of a part
+  static constexpr int pitch = 2 * C + 16;  // of a V row in LDS, bytes (below)
+};
 
 template <bool MX, int D>
 struct FewTile {
-  static constexpr int W = D / 32;  // words of codes per lane and row
-  uint32_t k[2][W], v[2][W];
-  uint32_t ks[2], vs[2];
+  typedef Few<D> F;
+  uint32_t k[2][F::P][F::W], v[2][F::P][F::W];
+  uint32_t ks[2][F::P], vs[2][F::P];  // words with the scale bytes
   int page[2];
 };
 
@@ -304,54 +324,50 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-// The scale bytes of a lane's D / 4 codes (segment g of the row).
-template <bool MX, int D>
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* row, int g) {
-  if constexpr (MX) {
-    if constexpr (D == 64) return row[g >> 1];
-    else if constexpr (D == 128) return row[g];
-    else return *reinterpret_cast<const uint16_t*>(row + 2 * g);
-  } else {
-    if constexpr (D == 64) return row[g];
-    else if constexpr (D == 128) return *reinterpret_cast<const uint16_t*>(row + 2 * g);
-    else return *reinterpret_cast<const uint32_t*>(row + 4 * g);
-  }
-}
-
-// Codes of 8-code word j of a lane's run lie in its scale block:
+// Word j of a run of codes that starts on a scale block lies in its block:
 template <bool MX>
 __device__ __forceinline__ constexpr int block_of_word(int j) {
   return MX ? j / 4 : j / 2;
 }
 
+// The scale bytes of a lane's C / 4 codes (row m of sixteen, segment g, part
+// p) lie in one aligned word: rows are loaded sixteen from a multiple of
+// sixteen, so that holds for rows of any number of bytes.  Byte offset.
 template <bool MX, int D>
-__device__ __forceinline__ void few_load(const Args& a, int h, int t0, int hi, const int (&page)[2],
+__device__ __forceinline__ constexpr int scale_byte(int m, int g, int p) {
+  constexpr int B = MX ? 32 : 16;
+  return m * (D / B) + (p * Few<D>::C + g * (Few<D>::C / 4)) / B;
+}
+
+template <bool MX, int D>
+__device__ __forceinline__ void few_load(const Args& a, int h, int t0, const int (&page)[2],
                                          FewTile<MX, D>& x) {
+  typedef Few<D> F;
   constexpr int B = MX ? 32 : 16;
   const int m = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+  // a lane's place in sixteen rows: 32-bit offsets from wave-uniform bases
+  const uint32_t code = m * (D / 2) + g * (F::C / 8);
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     x.page[r] = page[r];
     // sixteen tokens lie in one page; a page that the sequence does not have
     // is read as page 0 and its tokens are masked
-    const int64_t row = row_of(a, page[r], h, t0 + 16 * r) + m;
-    load_words(a.c.k_codes + row * (D / 2) + g * (D / 8), x.k[r]);
-    load_words(a.c.v_codes + row * (D / 2) + g * (D / 8), x.v[r]);
-    x.ks[r] = load_scales<MX, D>(a.c.k_scales + row * (D / B), g);
-    x.vs[r] = load_scales<MX, D>(a.c.v_scales + row * (D / B), g);
+    const int64_t row = row_of(a, page[r], h, t0 + 16 * r);
+#pragma unroll
+    for (int p = 0; p < F::P; ++p) {
+      const uint32_t scale = scale_byte<MX, D>(m, g, p) & ~3;
+      load_words(a.c.k_codes + row * (D / 2) + (code + p * (F::C / 2)), x.k[r][p]);
+      load_words(a.c.v_codes + row * (D / 2) + (code + p * (F::C / 2)), x.v[r][p]);
+      x.ks[r][p] = *reinterpret_cast<const uint32_t*>(a.c.k_scales + row * (D / B) + scale);
+      x.vs[r][p] = *reinterpret_cast<const uint32_t*>(a.c.v_scales + row * (D / B) + scale);
+    }
   }
 }
 
-// LDS place (bytes) of 16-byte piece p of row r of a wave's V tile: pieces
-// XOR-ed by the row so that the sixteen rows of a store phase (one piece)
-// and the eight rows of a transposing read's half wave (two pieces) reach
-// distinct banks.
-template <int D>
-__device__ __forceinline__ int few_at(int r, int p) {
-  const int s = D == 64 ? 2 * ((r >> 1) & 3) + ((r >> 3) & 1) : 2 * (r & 7) + ((r >> 3) & 1);
-  return r * (2 * D) + ((p ^ s) << 4);
-}
-
+// V's rows in LDS: sixteen bytes of padding keep the sixteen rows of a store
+// (one 16-byte piece of each) and the rows of a transposing read in distinct
+// banks (5.6 clocks a read instruction against 16 without; 4 is its least),
+// and every access of a lane is one address and a constant.
 __device__ __forceinline__ w2 read_tr16(const uint8_t* p) {
   return __builtin_bit_cast(w2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                     (__attribute__((address_space(3))) s16x4*)p));
@@ -371,166 +387,336 @@ __device__ __forceinline__ float max_over_g(float v) {
   return fmaxf(v, __shfl_xor(v, 32));
 }
 
-template <int D>
-constexpr int few_lds() {
-  constexpr int v = kFewWaves * kFewKeys * 2 * D;          // V tiles
-  constexpr int o = kFewWaves * 16 * (D + 4) * 4 + 1024;   // joining: outputs, (m, l)
-  return v > o ? v : o;
+// LDS of a workgroup: the waves' V tiles (later their results, to be joined),
+// q's fragments, each row's score scale, the waves' (m, l).
+template <bool LO, int D, int NT>
+struct FewLds {
+  typedef Few<D> F;
+  static constexpr int v = kFewWaves * kFewKeys * F::pitch;
+  static constexpr int o = kFewWaves * 16 * (F::C + 4) * 4;
+  static constexpr int q = v > o ? v : o;
+  static constexpr int q_part = NT * 16 * D * 2;  // high (or only) parts, then low parts
+  static constexpr int rs = q + q_part * (LO ? 2 : 1);
+  static constexpr int ml = rs + NT * 16 * 4;
+  static constexpr int bytes = ml + kFewWaves * 16 * 8;
+};
+
+// The list of work: every row tile of every sequence ("entry": sequence-major)
+// and every key head of it ("segment") has some tiles of keys; the tiles of
+// all segments in order are dealt to the workgroups in equal runs, whatever
+// the lengths.  A workgroup walks its run segment by segment.  A segment that
+// lies in one run is written out; of one that does not, each piece goes to a
+// slot of its workgroup: 2 g for the piece that its run begins with, 2 g + 1
+// for one that begins later (only its run's last piece can be cut), and
+// kv_few_join_kernel joins the pieces in the order of the list.  (With the
+// keys cut into equal pieces per sequence instead, 64 sequences of 2048 to
+// 8192 keys took 102 us at the best number of pieces; so 81.)
+// The host keeps the number of tiles under 2^31.
+struct Runs {
+  uint32_t per, more;  // tiles of a run; the first `more` runs have one more
+  __device__ __forceinline__ Runs(uint32_t total, uint32_t groups) {
+    per = total / groups;
+    more = total - per * groups;
+  }
+  __device__ __forceinline__ uint32_t begin(uint32_t g) const {
+    return g * per + (g < more ? g : more);
+  }
+  // the workgroup whose run holds tile x
+  __device__ __forceinline__ uint32_t of(uint32_t x) const {
+    const uint32_t cut = more * (per + 1);
+    return x < cut ? x / (per + 1) : more + (x - cut) / per;
+  }
+};
+
+template <int NT>
+struct Entry {
+  KvSeq s;
+  int seq, r0, r1;  // rows [r0, r1) of the sequence; none if r0 >= r1
+  Keys<kFewKeys> keys;
+  __device__ __forceinline__ void init(const Args& a, int e) {
+    seq = e / a.row_tiles;
+    s = kv_seq(a.b, seq, a.c.page_log2);
+    const int rows = s.n * a.group;
+    r0 = (e - seq * a.row_tiles) * (16 * NT);
+    r1 = r0 + 16 * NT < rows ? r0 + 16 * NT : rows;
+    keys.n = 0;
+    if (r0 < r1) keys.init(a, s, r0 / a.group, (r1 - 1) / a.group);
+  }
+};
+
+// Sum over the lanes before this one, and over all (DPP moves: no LDS trip).
+__device__ __forceinline__ uint32_t wave_sum_before(uint32_t v, uint32_t& all) {
+  uint32_t x = v;
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, false);  // row_shr:1
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, false);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, false);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, false);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false);  // row 0 -> 1, 2 -> 3
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false);  // rows 0-1 -> 2, 3
+  all = __builtin_amdgcn_readlane(x, 63);
+  return x - v;
 }
 
-template <bool MX, bool LO, int D, int NT>
-__global__ __launch_bounds__(kFewThreads, NT == 1 && D <= 128 ? 3 : 1) void kv_few_kernel(Args a) {
-  typedef Num<MX> N;
-  typedef typename N::x8 x8;
-  constexpr int W = D / 32;  // words of codes per lane = QK instructions
-  constexpr int J = D / 16;  // PV instructions (columns of 16)
-  __shared__ __align__(16) uint8_t lds[few_lds<D>()];
+__device__ __forceinline__ int64_t readlane64(int64_t v, int l) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, l);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(v >> 32), l);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
 
-  int id = blockIdx.x;
-  const int split = id % a.splits;
-  id /= a.splits;
-  const int rt = id % a.row_tiles;
-  id /= a.row_tiles;
-  const int h = id % a.c.heads, seq = id / a.c.heads;
-  const KvSeq s = kv_seq(a.b, seq, a.c.page_log2);
-  const int rows = s.n * a.group, r0 = rt * (16 * NT);
-  if (r0 >= rows) return;
-  const int r1 = r0 + 16 * NT < rows ? r0 + 16 * NT : rows;  // one past the last
-  Keys<kFewKeys> keys;
-  keys.init(a, s, r0 / a.group, (r1 - 1) / a.group, split);
-
-  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  uint8_t* vt = lds + wave * (kFewKeys * 2 * D);
-
-  // the lane's rows: query fragment, score scale, visible range
-  x8 qf[NT][W], ql[LO ? NT : 1][W];
-  float rs[NT];
-  int hi_row[NT], lo_row[NT];
-  const float sign = score_sign<MX>(a);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = r0 + 16 * n + m;
-    const bool has = r < r1;
-    const int i = (has ? r : r1 - 1) / a.group, head = h * a.group + (has ? r : r1 - 1) - i * a.group;
-    const uint16_t* q = a.q + (s.first + i) * a.q_token + head * a.q_head + g * (D / 4);
-    float t[D / 4], mx = 0.0f;
-#pragma unroll
-    for (int k = 0; k < D / 64; ++k) {
-      float x[16];
-      load_q16(q + 16 * k, a.c.rht, a.c.signs, x);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        t[16 * k + e] = x[e] * sign;
-        mx = fmaxf(mx, fabsf(x[e]));
-      }
+// Total tiles of the list, and the entry that holds the first tile of the
+// workgroup's run, with its number and the tiles before it.  Every wave does
+// this by itself, a lane per entry.
+template <int NT>
+__device__ __forceinline__ void find_run(const Args& a, int entries, uint32_t& total, int& entry,
+                                         uint32_t& before, Entry<NT>& at) {
+  const int lane = threadIdx.x & 63;
+  total = 0;
+  uint32_t mine = 0, ahead = 0, all;
+  Entry<NT> en;
+  auto look = [&](int e) {
+    mine = 0;
+    if (e < entries) {
+      en.init(a, e);
+      mine = (uint32_t)en.keys.n * a.c.heads;
     }
-    float down = 1.0f, up = 1.0f;
-    if constexpr (!MX) row_power(max_over_g(mx), down, up);
-    rs[n] = score_scale<MX>(a, up);
-    const int64_t p = s.pos + i;
-    hi_row[n] = (int)(p + 1 < 0 ? 0 : (p + 1 < s.kv ? p + 1 : s.kv));
-    lo_row[n] = a.window > 0 && p + 1 > a.window ? (int)(p + 1 - a.window < s.kv ? p + 1 - a.window : s.kv) : 0;
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      w4 w, x;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float u = t[8 * j + 2 * e] * down, v = t[8 * j + 2 * e + 1] * down;
-        w[e] = pack2<MX>(u, v);
-        if constexpr (LO)
-          x[e] = pack2<MX>(u - __uint_as_float(w[e] << 16), v - __uint_as_float(w[e] & 0xFFFF0000u));
-      }
-      qf[n][j] = as8<MX>(w);
-      if constexpr (LO) ql[n][j] = as8<MX>(x);
+  };
+  for (int base = 0; base < entries; base += 64) {
+    look(base + lane);
+    ahead = total + wave_sum_before(mine, all);
+    if (a.starts && blockIdx.x == 0 && threadIdx.x < 64 && base + lane < entries)
+      a.starts[base + lane] = ahead;
+    total += all;
+  }
+  if (a.starts && blockIdx.x == 0 && threadIdx.x == 0) a.starts[entries] = total;
+  entry = 0;
+  before = 0;
+  const uint32_t x = Runs(total, a.groups).begin(blockIdx.x);
+  uint32_t sum = 0;
+  for (int base = 0; base < entries; base += 64) {
+    if (entries > 64) {  // a list of more than 64 entries is walked again
+      look(base + lane);
+      ahead = sum + wave_sum_before(mine, all);
+      sum += all;
+    }
+    const uint64_t here = __ballot(x - ahead < mine);
+    if (here) {
+      const int l = __builtin_ctzll(here);
+      entry = base + l;
+      before = __builtin_amdgcn_readlane(ahead, l);
+      at.s.first = readlane64(en.s.first, l);
+      at.s.pos = readlane64(en.s.pos, l);
+      at.s.n = __builtin_amdgcn_readlane(en.s.n, l);
+      at.s.kv = __builtin_amdgcn_readlane(en.s.kv, l);
+      at.seq = __builtin_amdgcn_readlane(en.seq, l);
+      at.r0 = __builtin_amdgcn_readlane(en.r0, l);
+      at.r1 = __builtin_amdgcn_readlane(en.r1, l);
+      at.keys.sink_tiles = __builtin_amdgcn_readlane(en.keys.sink_tiles, l);
+      at.keys.start = __builtin_amdgcn_readlane(en.keys.start, l);
+      at.keys.n = __builtin_amdgcn_readlane(en.keys.n, l);
+      at.keys.lo = __builtin_amdgcn_readlane(en.keys.lo, l);
+      at.keys.hi = __builtin_amdgcn_readlane(en.keys.hi, l);
+      break;
     }
   }
+}
 
-  f32x4 o[NT][J], l[NT];
+// Rows of an entry that sees nothing: zeros.
+template <int NT>
+__device__ __forceinline__ void few_nothing(const Args& a, int64_t first, int r0, int r1) {
+  const int J = a.c.dim / 16;
+  const int rows = r1 - r0;
+  for (int k = threadIdx.x; k < rows * a.c.heads * J; k += kFewThreads) {
+    const int h = k / (rows * J), r = r0 + (k - h * (rows * J)) / J, d0 = (k % J) * 16;
+    const int i = r / a.group, head = h * a.group + r - i * a.group;
+    const float zero[16] = {};
+    store_out16(a, first + i, head, d0, zero);
+    if (a.lse && d0 == 0) a.lse[(first + i) * a.q_heads + head] = -__builtin_inff();
+  }
+}
+
+// The rows of q, rounded (and rotated), as the matrix instruction takes them:
+// part p, word j, lane (row m, segment g): columns p * C + g * C / 4 + 8 j ..
+// + 7 of row m.  A thread takes sixteen columns of a row.
+template <bool MX, bool LO, int D, int NT>
+__device__ __forceinline__ void few_query(const Args& a, const KvSeq& s, int h, int r0, int r1,
+                                          uint8_t* lds) {
+  typedef Few<D> F;
+  typedef FewLds<LO, D, NT> L;
+  constexpr int G = D / 16;  // threads of a row
+  const float sign = score_sign<MX>(a);
+#pragma unroll
+  for (int k = threadIdx.x; k < NT * 16 * G; k += kFewThreads) {
+    const int row = k / G, d = (k % G) * 16;
+    const int r = r0 + row < r1 ? r0 + row : r1 - 1;
+    const int i = r / a.group, head = h * a.group + r - i * a.group;
+    float x[16], mx = 0.0f;
+    load_q16(a.q + (s.first + i) * a.q_token + head * a.q_head + d, a.c.rht, a.c.signs, x);
+    float down = 1.0f, up = 1.0f;
+    if constexpr (!MX) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+      for (int o = 1; o < G; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+      row_power(mx, down, up);
+    }
+    if (d == 0) reinterpret_cast<float*>(lds + L::rs)[row] = score_scale<MX>(a, up);
+    down *= sign;
+    const int p = d / F::C, g = (d % F::C) / (F::C / 4), j0 = (d % (F::C / 4)) / 8;
+    uint8_t* to = lds + L::q + ((((row >> 4) * F::P + p) * F::W + j0) * 64 + g * 16 + (row & 15)) * 16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      w4 w, y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float u = x[8 * j + 2 * e] * down, v = x[8 * j + 2 * e + 1] * down;
+        w[e] = pack2<MX>(u, v);
+        if constexpr (LO)
+          y[e] = pack2<MX>(u - __uint_as_float(w[e] << 16), v - __uint_as_float(w[e] & 0xFFFF0000u));
+      }
+      *reinterpret_cast<w4*>(to + j * 1024) = w;
+      if constexpr (LO) *reinterpret_cast<w4*>(to + L::q_part + j * 1024) = y;
+    }
+  }
+}
+
+// Tiles [first, end) of a segment, into its rows' outputs (slot < 0) or a slot.
+template <bool MX, bool LO, int D, int NT>
+__device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, int h, int first,
+                                          int end, int64_t slot, uint8_t* lds) {
+  typedef Num<MX> N;
+  typedef typename N::x8 x8;
+  typedef Few<D> F;
+  typedef FewLds<LO, D, NT> L;
+  const KvSeq& s = en.s;
+  const Keys<kFewKeys>& keys = en.keys;
+  const int seq = en.seq, r0 = en.r0, r1 = en.r1;
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+
+  // A ring of tiles in registers: while one is worked on, the loads of the
+  // next R - 1 are in flight.  The loads are unconditional (past the last
+  // tile they read it again), so that the compiler can count them and wait
+  // for the oldest alone.
+  constexpr int R = few_ring(D);
+  FewTile<MX, D> ring[R];
+  const int last = end - 1;
+  int page[2];
+  auto pages_at = [&](int u) {
+    const int t = keys.base(u < last ? u : last);
+    page[0] = page_of(a, seq, t, keys.hi);
+    page[1] = page_of(a, seq, t + 16, keys.hi);
+  };
+  int u = first + wave;
+  pages_at(u);
+#pragma unroll
+  for (int k = 0; k < R - 1; ++k) {
+    const int v = u + k * kFewWaves;
+    few_load<MX, D>(a, h, keys.base(v < last ? v : last), page, ring[k]);
+    pages_at(v + kFewWaves);
+  }
+
+  few_query<MX, LO, D, NT>(a, s, h, r0, r1, lds);
+  __syncthreads();
+
+  // the lane's rows (16 n + m): score scale, visible range
+  float rs[NT];
+  int hi_row[NT], lo_row[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    rs[n] = reinterpret_cast<const float*>(lds + L::rs)[16 * n + m];
+    const int r = r0 + 16 * n + m < r1 ? r0 + 16 * n + m : r1 - 1;
+    const int64_t p = s.pos + r / a.group;
+    hi_row[n] = (int)(p + 1 < 0 ? 0 : (p + 1 < s.kv ? p + 1 : s.kv));
+    lo_row[n] = a.window > 0 && p + 1 > a.window ? (int)(p + 1 - a.window < s.kv ? p + 1 - a.window : s.kv) : 0;
+  }
+
+  f32x4 o[NT][F::P][F::J], l[NT];
   float top[NT];  // the row's running maximum, shared by its four lanes
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     top[n] = -__builtin_inff();
     l[n] = f32x4{};
 #pragma unroll
-    for (int j = 0; j < J; ++j) o[n][j] = f32x4{};
+    for (int p = 0; p < F::P; ++p)
+#pragma unroll
+      for (int j = 0; j < F::J; ++j) o[n][p][j] = f32x4{};
   }
   const x8 ones = as8<MX>(w4{N::kOnes, N::kOnes, N::kOnes, N::kOnes});
 
-  // rows of a transposing read: four tokens of the lane group, and the lane's
-  // place in them
-  const int tr_row = 4 * g + (m >> 2), tr_in = (m & 1) * 8, tr_piece = (m & 3) >> 1;
+  // the lane's place in a store of V (its token's row, its quarter) and in a
+  // transposing read (one of the four tokens of its lane group, four columns)
+  uint8_t* vt = lds + wave * (kFewKeys * F::pitch);
+  uint8_t* v_to = vt + m * F::pitch + g * (F::C / 2);
+  const uint8_t* v_from = vt + (4 * g + (m >> 2)) * F::pitch + (m & 3) * 8;
+  const uint8_t* q_from = lds + L::q + lane * 16;
   // keys that every row of this workgroup sees
   const int64_t p0 = s.pos + r0 / a.group, p1 = s.pos + (r1 - 1) / a.group;
   const int all_hi = (int)(p0 + 1 < 0 ? 0 : (p0 + 1 < s.kv ? p0 + 1 : s.kv));
   const int64_t all_lo = a.window > 0 ? p1 + 1 - a.window : 0;
 
-  FewTile<MX, D> cur, nxt;
-  int u = keys.begin + wave;
-  int page[2];
-  if (u < keys.end) {
-    const int t0 = keys.base(u);
-    page[0] = page_of(a, seq, t0, keys.hi);
-    page[1] = page_of(a, seq, t0 + 16, keys.hi);
-    few_load<MX, D>(a, h, t0, keys.hi, page, cur);
-    if (u + kFewWaves < keys.end) {
-      const int t1 = keys.base(u + kFewWaves);
-      page[0] = page_of(a, seq, t1, keys.hi);
-      page[1] = page_of(a, seq, t1 + 16, keys.hi);
-    }
-  }
-  for (; u < keys.end; u += kFewWaves) {
-    const int t0 = keys.base(u);
-    if (u + kFewWaves < keys.end) {
-      few_load<MX, D>(a, h, keys.base(u + kFewWaves), keys.hi, page, nxt);
-      if (u + 2 * kFewWaves < keys.end) {
-        const int t2 = keys.base(u + 2 * kFewWaves);
-        page[0] = page_of(a, seq, t2, keys.hi);
-        page[1] = page_of(a, seq, t2 + 16, keys.hi);
-      }
-    }
+  auto work = [&](FewTile<MX, D>& cur, int t0) {
     const bool inside = t0 + kFewKeys <= all_hi && t0 >= all_lo && cur.page[0] >= 0 && cur.page[1] >= 0;
     if (!inside) {
       // what no row sees may hold anything (it was never written, or its
       // page was given back): its codes and scales become zeros, so that
       // a probability of 0 meets no NaN
+      int tm = t0 + m;
+      asm volatile("" : "+v"(tm));  // a branch: most tiles skip this
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int t = t0 + 16 * r + m;
+        const int t = tm + 16 * r;
         const bool ok = cur.page[r] >= 0 && t < keys.hi && (t >= keys.lo || t < a.sinks);
 #pragma unroll
-        for (int j = 0; j < W; ++j) cur.v[r][j] = ok ? cur.v[r][j] : 0u;
-        cur.vs[r] = ok ? cur.vs[r] : 0u;
+        for (int p = 0; p < F::P; ++p) {
+#pragma unroll
+          for (int j = 0; j < F::W; ++j) cur.v[r][p][j] = ok ? cur.v[r][p][j] : 0u;
+          cur.vs[r][p] = ok ? cur.vs[r][p] : 0u;
+        }
       }
     }
-    // S^T = K q^T: registers i of tile r: key t0 + 16 r + 4 g + i
+    // S^T = K q^T: register i of tile r: key t0 + 16 r + 4 g + i
     f32x4 sc[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = f32x4{};
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int p = 0; p < F::P; ++p) {
+      const int shift = (scale_byte<MX, D>(m, g, p) & 3) * 8;
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        Scale<MX> k;
-        block_scale(cur.ks[r], block_of_word<MX>(j), k);
-        const x8 kf = as8<MX>(dequant8(cur.k[r][j], k));
+      for (int j = 0; j < F::W; ++j) {
+        x8 qf[NT], ql[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          sc[n][r] = N::mma(kf, qf[n][j], sc[n][r]);
-          if constexpr (LO) sc[n][r] = N::mma(kf, ql[n][j], sc[n][r]);
+          const uint8_t* q = q_from + ((n * F::P + p) * F::W + j) * 1024;
+          qf[n] = as8<MX>(*reinterpret_cast<const w4*>(q));
+          if constexpr (LO) ql[n] = as8<MX>(*reinterpret_cast<const w4*>(q + L::q_part));
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          Scale<MX> k;
+          block_scale(cur.ks[r][p] >> shift, block_of_word<MX>(j), k);
+          const x8 kf = as8<MX>(dequant8(cur.k[r][p][j], k));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            sc[n][r] = N::mma(kf, qf[n], sc[n][r]);
+            if constexpr (LO) sc[n][r] = N::mma(kf, ql[n], sc[n][r]);
+          }
         }
       }
-    // V's rows to LDS
-    wave_lds_fence();
+    }
+    auto store_v = [&](int p) {
+      const int shift = (scale_byte<MX, D>(m, g, p) & 3) * 8;
+      wave_lds_fence();
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        Scale<MX> k;
-        block_scale(cur.vs[r], block_of_word<MX>(j), k);
-        *reinterpret_cast<w4*>(vt + few_at<D>(16 * r + m, g * W + j)) = dequant8(cur.v[r][j], k);
-      }
-    wave_lds_fence();
+        for (int j = 0; j < F::W; ++j) {
+          Scale<MX> k;
+          block_scale(cur.vs[r][p] >> shift, block_of_word<MX>(j), k);
+          *reinterpret_cast<w4*>(v_to + 16 * r * F::pitch + 16 * j) = dequant8(cur.v[r][p][j], k);
+        }
+      wave_lds_fence();
+    };
+    store_v(0);
 
     x8 pf[NT];
 #pragma unroll
@@ -541,11 +727,13 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 && D <= 128 ? 3 : 1) void kv_f
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[4 * r + i] = sc[n][r][i];
       if (!inside) {
+        int tg = t0 + 4 * g;
+        asm volatile("" : "+v"(tg));  // a branch: most tiles skip this
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int t = t0 + 16 * r + 4 * g + i;
+            const int t = tg + 16 * r + i;
             const bool seen = cur.page[r] >= 0 && t < hi_row[n] && (t >= lo_row[n] || t < a.sinks);
             v[4 * r + i] = seen ? v[4 * r + i] : -__builtin_inff();
           }
@@ -564,7 +752,9 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 && D <= 128 ? 3 : 1) void kv_f
         top[n] = t;
         l[n] *= f;
 #pragma unroll
-        for (int j = 0; j < J; ++j) o[n][j] *= f;
+        for (int p = 0; p < F::P; ++p)
+#pragma unroll
+          for (int j = 0; j < F::J; ++j) o[n][p][j] *= f;
       }
       const float sub = top[n] == -__builtin_inff() ? 0.0f : top[n];
       w4 w;
@@ -578,33 +768,49 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 && D <= 128 ? 3 : 1) void kv_f
     // O^T += V^T P^T: contraction slots (g, i): key t0 + 4 g + i, then t0 +
     // 16 + 4 g + i - 4
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int at = few_at<D>(tr_row, 2 * j + tr_piece) + tr_in;
-      const w2 x = read_tr16(vt + at), y = read_tr16(vt + at + 16 * 2 * D);
-      const x8 vf = as8<MX>(w4{x.x, x.y, y.x, y.y});
+    for (int p = 0; p < F::P; ++p) {
+      if (p) store_v(p);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) o[n][j] = N::mma(vf, pf[n], o[n][j]);
+      for (int j = 0; j < F::J; ++j) {
+        const w2 x = read_tr16(v_from + 32 * j), y = read_tr16(v_from + 32 * j + 16 * F::pitch);
+        const x8 vf = as8<MX>(w4{x.x, x.y, y.x, y.y});
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[n][p][j] = N::mma(vf, pf[n], o[n][p][j]);
+      }
     }
-    cur = nxt;
+  };
+  while (u < end) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (u < end) {
+        const int v = u + (R - 1) * kFewWaves;
+        few_load<MX, D>(a, h, keys.base(v < last ? v : last), page, ring[(k + R - 1) % R]);
+        pages_at(v + kFewWaves);
+        work(ring[k], keys.base(u));
+      }
+      u += kFewWaves;
+    }
   }
 
-  // Join the four waves: every wave's rows and (m, l) through LDS, then a
-  // thread per row and 16 columns.
-  constexpr int P = D + 4;  // row pitch, floats
+  // Join the four waves, a part of the columns at a time: every wave's rows
+  // and (m, l) through LDS, then a thread per row and 16 columns.
+  constexpr int pitch = F::C + 4;  // floats
   float* om = reinterpret_cast<float*>(lds);
-  float2* ml = reinterpret_cast<float2*>(lds + few_lds<D>() - 1024);
-  for (int n = 0; n < NT; ++n) {
+  float2* ml = reinterpret_cast<float2*>(lds + L::ml);
+#pragma unroll 1
+  for (int np = 0; np < NT * F::P; ++np) {
+    const int n = np / F::P, part = np - n * F::P;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < NT; ++k)
-      if (k == n) {
+    for (int k = 0; k < NT * F::P; ++k)
+      if (k == np) {
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-          *reinterpret_cast<f32x4*>(om + (wave * 16 + m) * P + 16 * j + 4 * g) = o[k][j];
-        if (g == 0) ml[wave * 16 + m] = make_float2(top[k], l[k][0]);
+        for (int j = 0; j < F::J; ++j)
+          *reinterpret_cast<f32x4*>(om + (wave * 16 + m) * pitch + 16 * j + 4 * g) = o[k / F::P][k % F::P][j];
+        if (g == 0) ml[wave * 16 + m] = make_float2(top[k / F::P], l[k / F::P][0]);
       }
     __syncthreads();
-    const int row = threadIdx.x / J, d0 = (threadIdx.x % J) * 16;
+    const int row = threadIdx.x / F::J, c0 = (threadIdx.x % F::J) * 16, d0 = part * F::C + c0;
     const int r = r0 + 16 * n + row;
     if (row >= 16 || r >= r1) continue;
     float t = -__builtin_inff();
@@ -618,11 +824,11 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 && D <= 128 ? 3 : 1) void kv_f
       const float f = __builtin_amdgcn_exp2f(e.x - sub);
       sum += e.y * f;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] += om[(w * 16 + row) * P + d0 + k] * f;
+      for (int k = 0; k < 16; ++k) x[k] += om[(w * 16 + row) * pitch + c0 + k] * f;
     }
-    const int i = r / a.group, head = h * a.group + r - i * a.group;
-    const int64_t token = s.first + i;
-    if (a.splits == 1) {
+    if (slot < 0) {
+      const int i = r / a.group, head = h * a.group + r - i * a.group;
+      const int64_t token = s.first + i;
       const float f = out_factor<MX>(a, sum);
 #pragma unroll
       for (int k = 0; k < 16; ++k) x[k] *= f;
@@ -630,14 +836,54 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 && D <= 128 ? 3 : 1) void kv_f
       store_out16(a, token, head, d0, x);
       if (a.lse && d0 == 0) a.lse[token * a.q_heads + head] = row_lse(t, sum);
     } else {
-      const int64_t at = ((int64_t)split * a.b.tokens + token) * a.q_heads + head;
+      const int64_t at = slot * (16 * NT) + 16 * n + row;
       if (d0 == 0) a.part_ml[at] = make_float2(t, sum);
-      if (sum > 0.0f) {
-        f32x4* p = reinterpret_cast<f32x4*>(a.part + at * D + d0);
+      f32x4* p = reinterpret_cast<f32x4*>(a.part + at * D + d0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = f32x4{x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]};
-      }
+      for (int k = 0; k < 4; ++k) p[k] = f32x4{x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]};
     }
+  }
+}
+
+template <bool MX, bool LO, int D, int NT>
+__global__ __launch_bounds__(kFewThreads, few_residents(D, 16 * NT)) void kv_few_kernel(Args a) {
+  __shared__ __align__(16) uint8_t lds[FewLds<LO, D, NT>::bytes];
+  const int entries = a.b.batch * a.row_tiles;
+  uint32_t total, before;
+  int e;
+  Entry<NT> en;
+  find_run<NT>(a, entries, total, e, before, en);
+  const Runs runs(total, a.groups);
+  const uint32_t x0 = runs.begin(blockIdx.x), x1 = runs.begin(blockIdx.x + 1);
+  uint32_t x = x0;
+  // Entries that see nothing have no tiles: the workgroup that ends the entry
+  // before them writes their zeros, the first one those at the beginning.
+  bool known = x < x1;
+  if (blockIdx.x == 0) {
+    if (e > 0 || !known) known = false, e = 0, before = 0;
+  } else if (!known) {
+    return;
+  }
+  for (; e < entries; ++e) {
+    if (!known) en.init(a, e);
+    known = false;
+    const uint32_t n = en.keys.n;
+    if (n == 0) {
+      if (en.r0 < en.r1) few_nothing<NT>(a, en.s.first, en.r0, en.r1);
+      continue;
+    }
+    if (x >= x1) return;
+    const uint32_t here = n * a.c.heads;
+    while (x < x1 && x - before < here) {
+      const int h = (int)((x - before) / n), t = (int)((x - before) - h * n);
+      const int len = (int)(x1 - x < n - t ? x1 - x : n - t);
+      const int64_t slot = len == (int)n ? -1 : 2 * (int64_t)blockIdx.x + (x != x0);
+      few_piece<MX, LO, D, NT>(a, en, h, t, t + len, slot, lds);
+      x += len;
+      if (x < x1) __syncthreads();  // the LDS of the joined waves is the next piece's
+    }
+    if (x - before < here) return;
+    before += here;
   }
 }
 
@@ -651,6 +897,20 @@ constexpr int kManyThreads = 512, kManyRows = 256, kManyKeys = 64;
 // LDS places of 16-byte piece p of row r.  K is read by 32 rows at one piece,
 // V through the transposing read: four rows of two pairs of pieces to a half
 // wave; both are written four rows and four pieces (every W-th) at a time.
+// The scale bytes of a quarter (segment g) of a row.
+template <bool MX, int D>
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* row, int g) {
+  if constexpr (MX) {
+    if constexpr (D == 64) return row[g >> 1];
+    else if constexpr (D == 128) return row[g];
+    else return *reinterpret_cast<const uint16_t*>(row + 2 * g);
+  } else {
+    if constexpr (D == 64) return row[g];
+    else if constexpr (D == 128) return *reinterpret_cast<const uint16_t*>(row + 2 * g);
+    else return *reinterpret_cast<const uint32_t*>(row + 4 * g);
+  }
+}
+
 template <int D>
 __device__ __forceinline__ int many_k_at(int r, int p) {
   const int s = D == 64 ? (r >> 1) & 7 : r & 15;
@@ -722,7 +982,14 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv_many_kernel(Args a) {
   if (r0 >= rows) return;
   const int r1 = r0 + kManyRows < rows ? r0 + kManyRows : rows;
   Keys<kManyKeys> keys;
-  keys.init(a, s, r0 / a.group, (r1 - 1) / a.group, split);
+  keys.init(a, s, r0 / a.group, (r1 - 1) / a.group);
+  // every split takes as many tiles whatever the sequence (the host sizes
+  // them by the longest list); a list past that bound is shared evenly
+  const int bound = (int)(max_keys(a.b.max_kv, a.window, a.sinks, a.b.max_q) / kManyKeys) + 3;
+  const int per = ((keys.n > bound ? keys.n : bound) + a.splits - 1) / a.splits;
+  const int64_t from = (int64_t)split * per;
+  const int begin = from < keys.n ? (int)from : keys.n;
+  const int end = from + per < keys.n ? (int)(from + per) : keys.n;
 
   const int lane = threadIdx.x & 63, half = lane >> 5, qrow = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -825,13 +1092,13 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv_many_kernel(Args a) {
 
   // tiles without a page (the sequence gave it back) hold zeros, which are
   // not keys: their scores are masked by the page table in the masked path
-  if (keys.begin < keys.end) {
-    fetch(keys.base(keys.begin));
+  if (begin < end) {
+    fetch(keys.base(begin));
     stage(0);
   }
-  for (int u = keys.begin; u < keys.end; ++u) {
-    const int t0 = keys.base(u), buf = (u - keys.begin) & 1;
-    if (u + 1 < keys.end) fetch(keys.base(u + 1));
+  for (int u = begin; u < end; ++u) {
+    const int t0 = keys.base(u), buf = (u - begin) & 1;
+    if (u + 1 < end) fetch(keys.base(u + 1));
     __syncthreads();
     const uint8_t* kt = lds + buf * 2 * kTile;
     const uint8_t* vt = kt + kTile;
@@ -910,7 +1177,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv_many_kernel(Args a) {
         }
       }
     }
-    if (u + 1 < keys.end) stage(buf ^ 1);
+    if (u + 1 < end) stage(buf ^ 1);
   }
 
   if (!works || w0 + qrow >= r1) return;
@@ -1002,18 +1269,96 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(Args a) {
   if (a.lse && d0 == 0) a.lse[row] = row_lse(t, l);
 }
 
+// The pieces of a segment of few rows: a wave per segment and row, D / 4
+// lanes to a piece (four columns each), the pieces dealt to the wave's slots
+// in order and the slots summed in a fixed order.
+constexpr int kFewJoinWaves = 4;
+
+template <bool MX, int D, int NT>
+__global__ __launch_bounds__(64 * kFewJoinWaves) void kv_few_join_kernel(Args a) {
+  constexpr int C = D / 4, SL = 64 / C;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int e = blockIdx.y, job = blockIdx.x * kFewJoinWaves + wave;
+  const int h = job / a.join_rows, row = job - h * a.join_rows;
+  if (h >= a.c.heads) return;
+  const int seq = e / a.row_tiles;
+  const KvSeq s = kv_seq(a.b, seq, a.c.page_log2);
+  const uint32_t total = a.starts[a.b.batch * a.row_tiles], begin = a.starts[e];
+  const uint32_t tiles = a.starts[e + 1] - begin;
+  const int r = (e - seq * a.row_tiles) * (16 * NT) + row;
+  if (tiles == 0 || r >= s.n * a.group) return;
+  const Runs runs(total, a.groups);
+  const uint32_t n = tiles / a.c.heads, x = begin + h * n;
+  const int g0 = runs.of(x), g1 = runs.of(x + n - 1);
+  if (g0 == g1) return;  // one workgroup had it all
+  const int c = lane % C, sl = lane / C;
+  const int64_t first = 2 * (int64_t)g0 + (runs.begin(g0) != x);
+  auto at = [&](int g) { return (g == g0 ? first : 2 * (int64_t)g) * (16 * NT) + row; };
+  float top = -__builtin_inff(), l = 0.0f;
+  for (int g = g0 + lane; g <= g1; g += 64) top = fmaxf(top, a.part_ml[at(g)].x);
+  top = wave_max(top);
+  const float sub = top == -__builtin_inff() ? 0.0f : top;
+  f32x4 v = {};
+#pragma unroll 8  // loads in flight
+  for (int g = g0 + sl; g <= g1; g += SL) {
+    const int64_t p = at(g);
+    const float2 q = a.part_ml[p];
+    const float f = __builtin_amdgcn_exp2f(q.x - sub);
+    l += q.y * f;
+    v += *reinterpret_cast<const f32x4*>(a.part + p * D + 4 * c) * f;
+  }
+#pragma unroll
+  for (int o = C; o < 64; o <<= 1) {
+    l += __shfl_xor(l, o);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += __shfl_xor(v[k], o);
+  }
+  v *= out_factor<MX>(a, l);
+  if (a.c.rht) {  // columns 4 c .. 4 c + 3 of a 16-group: lanes 1 and 2 apart hold the others
+    float y[4] = {v[0] + v[1], v[0] - v[1], v[2] + v[3], v[2] - v[3]};
+    v = f32x4{y[0] + y[2], y[1] + y[3], y[0] - y[2], y[1] - y[3]};
+#pragma unroll
+    for (int st = 1; st < 4; st <<= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float other = __shfl_xor(v[k], st);
+        v[k] = (c & st) ? other - v[k] : v[k] + other;
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float y4 = v[k] * 0.25f;
+      v[k] = ((a.c.signs >> (4 * (c & 3) + k)) & 1u) ? -y4 : y4;
+    }
+  }
+  if (lane >= C) return;
+  const int i = r / a.group, head = h * a.group + r - i * a.group;
+  const int64_t token = s.first + i, to = token * a.out_token + head * a.out_head + 4 * c;
+  if (a.out_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + to) = v;
+  else
+    *reinterpret_cast<w2*>(static_cast<uint16_t*>(a.out) + to) = w2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+  if (a.lse && c == 0) a.lse[token * a.q_heads + head] = row_lse(top, l);
+}
+
 // ===================================================================== host
+template <bool MX, bool LO, int D, int NT>
+hipError_t launch_few(const Args& a, hipStream_t s) {
+  kv_few_kernel<MX, LO, D, NT><<<(unsigned)a.groups, kFewThreads, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.groups == 1) return e;
+  const dim3 grid((unsigned)((a.c.heads * a.join_rows + kFewJoinWaves - 1) / kFewJoinWaves),
+                  (unsigned)(a.b.batch * a.row_tiles));
+  kv_few_join_kernel<MX, D, NT><<<grid, 64 * kFewJoinWaves, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <bool MX, bool LO, int D>
 hipError_t launch_d(const Args& a, const KvAttentionPlan& p, hipStream_t s) {
-  const int64_t groups = (int64_t)a.b.batch * a.c.heads * p.row_tiles * p.splits;
-  if (p.prompt) {
-    kv_many_kernel<MX, LO, D><<<(unsigned)groups, kManyThreads, 0, s>>>(a);
-  } else if (p.rows == 16) {
-    kv_few_kernel<MX, LO, D, 1><<<(unsigned)groups, kFewThreads, 0, s>>>(a);
-  } else {
-    kv_few_kernel<MX, LO, D, 2><<<(unsigned)groups, kFewThreads, 0, s>>>(a);
-  }
-  hipError_t e = hipGetLastError();
+  if (!p.prompt)
+    return p.rows == 16 ? launch_few<MX, LO, D, 1>(a, s)
+                        : launch_few<MX, LO, D, D <= 128 ? 2 : 1>(a, s);
+  kv_many_kernel<MX, LO, D><<<(unsigned)p.groups, kManyThreads, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 grid((unsigned)a.b.max_q * (unsigned)a.q_heads, (unsigned)a.b.batch);
   kv_join_kernel<MX, D><<<grid, kJoinThreads, 0, s>>>(a);
@@ -1036,22 +1381,33 @@ KvAttentionPlan fp4_plan_kv_attention(const KvCacheArgs& c, const KvBatchArgs& b
   KvAttentionPlan p{};
   const int64_t rows = (int64_t)b.max_q * (q_heads / c.heads);
   p.prompt = rows > 64;
-  p.rows = p.prompt ? kManyRows : (rows > 16 ? 32 : 16);
+  // 32 rows of 256 columns would leave a compute unit one workgroup
+  p.rows = p.prompt ? kManyRows : (rows > 16 && c.dim <= 128 ? 32 : 16);
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
-  int64_t seen = b.max_kv;
-  if (window > 0 && (int64_t)window + sinks + b.max_q < seen) seen = (int64_t)window + sinks + b.max_q;
-  const int tile = p.prompt ? kManyKeys : kFewKeys;
-  const int64_t tiles = (seen + tile - 1) / tile + 2;
-  const int64_t groups = (int64_t)b.batch * c.heads * p.row_tiles;
-  // enough workgroups to fill the chip, and tiles enough for each
-  const int64_t want = p.prompt ? 512 : 1024;
-  const int64_t least = p.prompt ? 8 : 8;  // tiles of a split at least
-  int64_t n = groups > 0 ? want / groups : 1;
-  if (n > tiles / least) n = tiles / least;
-  if (n < 1) n = 1;
-  if (n > 256) n = 256;
-  p.splits = (int)n;
-  if (n > 1) p.bytes = (size_t)(n * b.tokens * q_heads) * ((size_t)c.dim * 4 + 8);
+  const int64_t seen = max_keys(b.max_kv, window, sinks, b.max_q);
+  const int64_t segments = (int64_t)b.batch * c.heads * p.row_tiles;
+  if (p.prompt) {
+    // pieces of the keys where the row tiles alone do not fill the chip, of
+    // at least eight tiles
+    const int64_t tiles = seen / kManyKeys + 3;
+    int64_t n = segments > 0 ? 512 / segments : 1;
+    if (n > tiles / 8) n = tiles / 8;
+    p.splits = (int)(n < 1 ? 1 : n);
+    p.groups = segments * p.splits;
+    if (p.splits > 1) p.bytes = (size_t)(p.splits * b.tokens * q_heads) * ((size_t)c.dim * 4 + 8);
+    return p;
+  }
+  // as many workgroups as the chip holds at once; fewer where a run would be
+  // shorter than a tile for each wave
+  const int64_t resident = 256 * few_residents(c.dim, p.rows);
+  const int64_t tiles = segments * (seen / kFewKeys + 2);
+  int64_t n = tiles / kFewLeast;
+  if (n > resident) n = resident;
+  p.splits = 1;
+  p.groups = n < 1 ? 1 : n;
+  if (p.groups > 1)
+    p.bytes = (size_t)p.groups * 2 * p.rows * ((size_t)c.dim * 4 + 8) +
+              ((size_t)b.batch * p.row_tiles + 1) * 4;
   return p;
 }
 
@@ -1074,11 +1430,16 @@ hipError_t fp4_launch_kv_attention(const KvAttentionLaunch& q, hipStream_t s) {
   a.out_head = q.out_head;
   a.lse = q.lse;
   a.splits = p.splits;
+  a.groups = (int)p.groups;
   a.row_tiles = p.row_tiles;
-  if (p.splits > 1) {
-    const int64_t rows = (int64_t)p.splits * q.batch.tokens * q.q_heads;
+  const int64_t rows_of_tile = (int64_t)q.batch.max_q * a.group;
+  a.join_rows = (int)(rows_of_tile < p.rows ? rows_of_tile : p.rows);
+  if (p.bytes) {
+    const int64_t rows = p.prompt ? (int64_t)p.splits * q.batch.tokens * q.q_heads
+                                  : p.groups * 2 * p.rows;
     a.part = static_cast<float*>(q.workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + rows * q.cache.dim);
+    if (!p.prompt) a.starts = reinterpret_cast<uint32_t*>(a.part_ml + rows);
   }
   if (q.cache.format == kNVFP4) return launch<false, false>(a, p, s);
   return q.cache.rht ? launch<true, true>(a, p, s) : launch<true, false>(a, p, s);
