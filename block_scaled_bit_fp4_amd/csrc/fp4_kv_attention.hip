@@ -79,6 +79,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, typename Num<MX>::x2));
 }
 
+// l + both of a packed pair, in binary32.
+template <bool MX>
+__device__ __forceinline__ float add_pair(uint32_t w, float l) {
+  typedef typename Num<MX>::x2 x2;
+  const x2 v = __builtin_bit_cast(x2, w), one = __builtin_bit_cast(x2, Num<MX>::kOnes);
+  if constexpr (MX) return __builtin_amdgcn_fdot2_f32_bf16(v, one, l, false);
+  else return __builtin_amdgcn_fdot2(v, one, l, false);
+}
+
 template <bool MX>
 __device__ __forceinline__ typename Num<MX>::x8 as8(const w4& w) {
   return __builtin_bit_cast(typename Num<MX>::x8, w);
@@ -312,7 +321,9 @@ struct FewTile {
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
-  if constexpr (N == 2) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
     const w2 t = *reinterpret_cast<const w2*>(p);
     w[0] = t.x; w[1] = t.y;
   } else {
@@ -888,29 +899,25 @@ __global__ __launch_bounds__(kFewThreads, few_residents(D, 16 * NT)) void kv_few
 }
 
 // ============================================================ many new tokens
-// 256 rows to a workgroup of eight waves, 32 rows to a wave, tiles of 64
-// keys: the workgroup dequantizes a tile once into LDS (K and V, 16 bits),
-// while the waves work on the tile before it; every wave takes its products
-// from there.
-constexpr int kManyThreads = 512, kManyRows = 256, kManyKeys = 64;
+// Waves of 32 rows each (eight of them, four for 256 columns) share tiles of
+// 64 keys, dequantized once into LDS (K and V, 16 bits, two tiles of each).
+//
+// Bound by issue: a score costs 4 * D matrix flops and about nine vector
+// instructions with the staging's share, one of them a quarter-rate exp2, so
+// the vector unit is as busy as the matrix unit.  Three steps of the work run
+// side by side on sub-tiles of 32 keys, in an order that is written out: the
+// scores of the next, the exponentials of this, the output of the one before,
+// with one barrier a tile.  Two waves to a SIMD fill each other's gaps (one,
+// of 64 rows, halves the LDS reads but leaves every wait open: 454 us for two
+// prompts of 4096 tokens against 384); of 256 columns only one fits.
+constexpr int kManyKeys = 64;
+
+__host__ __device__ constexpr int many_waves(int dim) { return dim <= 128 ? 8 : 4; }
+__host__ __device__ constexpr int many_rows(int dim) { return 32 * many_waves(dim); }
 
 // LDS places of 16-byte piece p of row r.  K is read by 32 rows at one piece,
 // V through the transposing read: four rows of two pairs of pieces to a half
 // wave; both are written four rows and four pieces (every W-th) at a time.
-// The scale bytes of a quarter (segment g) of a row.
-template <bool MX, int D>
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* row, int g) {
-  if constexpr (MX) {
-    if constexpr (D == 64) return row[g >> 1];
-    else if constexpr (D == 128) return row[g];
-    else return *reinterpret_cast<const uint16_t*>(row + 2 * g);
-  } else {
-    if constexpr (D == 64) return row[g];
-    else if constexpr (D == 128) return *reinterpret_cast<const uint16_t*>(row + 2 * g);
-    else return *reinterpret_cast<const uint32_t*>(row + 4 * g);
-  }
-}
-
 template <int D>
 __device__ __forceinline__ int many_k_at(int r, int p) {
   const int s = D == 64 ? (r >> 1) & 7 : r & 15;
@@ -959,15 +966,18 @@ __device__ __forceinline__ void rotate_back32(f32x16& v, int half, uint32_t sign
 }
 
 template <bool MX, bool LO, int D>
-__global__ __launch_bounds__(kManyThreads, 2) void kv_many_kernel(Args a) {
+__global__ __launch_bounds__(64 * many_waves(D), many_waves(D) / 4) void kv_many_kernel(Args a) {
   typedef Num<MX> N;
   typedef typename N::x8 x8;
   constexpr int B = MX ? 32 : 16;
-  constexpr int W = D / 32;      // words of codes of a thread's quarter row
-  constexpr int QK = D / 16;     // S^T instructions of one 32-key tile
+  constexpr int kWaves = many_waves(D), kManyThreads = 64 * kWaves;
+  constexpr int SEG = kWaves;    // threads to a row of a tile in staging
+  constexpr int W = D / (8 * SEG);  // words of codes of such a piece
+  constexpr int QK = D / 16;     // S^T instructions of a sub-tile and 32 rows
   constexpr int DT = D / 32;     // 32-column tiles of the output
+  constexpr int kRows = many_rows(D);
   constexpr int kTile = kManyKeys * 2 * D;  // bytes of one tile of K or V
-  __shared__ __align__(16) uint8_t lds[4 * kTile];  // two tiles of K and of V
+  __shared__ __align__(16) uint8_t lds[4 * kTile];  // K, K, V, V
 
   // row tiles with the most keys first: the last workgroups to run are short
   int id = blockIdx.x;
@@ -978,9 +988,9 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv_many_kernel(Args a) {
   const int split = id % a.splits;
   const int rt = a.row_tiles - 1 - id / a.splits;
   const KvSeq s = kv_seq(a.b, seq, a.c.page_log2);
-  const int rows = s.n * a.group, r0 = rt * kManyRows;
+  const int rows = s.n * a.group, r0 = rt * kRows;
   if (r0 >= rows) return;
-  const int r1 = r0 + kManyRows < rows ? r0 + kManyRows : rows;
+  const int r1 = r0 + kRows < rows ? r0 + kRows : rows;
   Keys<kManyKeys> keys;
   keys.init(a, s, r0 / a.group, (r1 - 1) / a.group);
   // every split takes as many tiles whatever the sequence (the host sizes
@@ -993,226 +1003,381 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv_many_kernel(Args a) {
 
   const int lane = threadIdx.x & 63, half = lane >> 5, qrow = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  // this wave's rows
-  const int w0 = r0 + 32 * wave;
+  const int w0 = r0 + 32 * wave;  // this wave's rows: w0 .. w1 - 1
   const bool works = w0 < r1;
   const int w1 = w0 + 32 < r1 ? w0 + 32 : r1;
-  const int r = works ? (w0 + qrow < r1 ? w0 + qrow : r1 - 1) : r0;
-  const int qi = r / a.group, head = h * a.group + r - qi * a.group;
 
-  x8 qf[QK], ql[LO ? QK : 1];
-  float rs;
-  {
-    const uint16_t* q = a.q + (s.first + qi) * a.q_token + head * a.q_head;
-    const float sign = score_sign<MX>(a);
-    float mx = 0.0f, down = 1.0f, up = 1.0f;
-    // a lane keeps columns 16 j + 8 half + 0..7; the rotation takes whole
-    // 16-groups, which both halves compute
-    if constexpr (!MX) {
+  // Staging: SEG threads to a row, a piece (D / SEG codes) of K and of V each;
+  // a wave's rows lie in one page.
+  const int st_row = threadIdx.x / SEG, st_seg = threadIdx.x % SEG;
+  constexpr int kRowsOfWave = 64 / SEG;
+  struct Raw {
+    uint32_t k[W], v[W], ks, vs;
+  };
+  const int last = end - 1;
+  // a lane's place in the sixteen rows that its wave's rows are among
+  const int st_in = st_row & 15;
+  const uint32_t st_code = st_in * (D / 2) + st_seg * (D / (2 * SEG)), st_byte = st_in * (D / B) + st_seg * (D / SEG) / B;
+  const int st_shift = (st_byte & 3) * 8;  // the piece's scale bytes lie in one aligned word
+  const uint8_t* kc = a.c.k_codes + ((int64_t)h << a.c.page_log2) * (D / 2) + st_code;
+  const uint8_t* vc = a.c.v_codes + ((int64_t)h << a.c.page_log2) * (D / 2) + st_code;
+  const uint8_t* ks = a.c.k_scales + ((int64_t)h << a.c.page_log2) * (D / B) + (st_byte & ~3u);
+  const uint8_t* vs = a.c.v_scales + ((int64_t)h << a.c.page_log2) * (D / B) + (st_byte & ~3u);
+  const uint32_t page_bytes = ((uint32_t)a.c.heads << a.c.page_log2) * (D / 2);
+  // Pages of the four sixteens of a tile, in lanes 0 to 3 (and again in
+  // every four after them), loaded a tile ahead of their use; -1: none.
+  auto pages_at = [&](int u) __attribute__((always_inline)) {
+    const int t = keys.base(u < last ? u : last) + 16 * (lane & 3);
+    const int64_t at = seq * a.b.table_ld + ((t < keys.hi ? t : 0) >> a.c.page_log2);
+    const int p = a.b.page_table[at];
+    return t < keys.hi && p >= 0 && p < a.c.pages ? p : -1;
+  };
+  auto fetch = [&](int u, int pages, Raw& x) __attribute__((always_inline)) {
+    const int t0 = keys.base(u < last ? u : last);
+    const int sixteen = wave * kRowsOfWave / 16;
+    const int page = __builtin_amdgcn_readlane(pages, sixteen);
+    // the place of the sixteen rows (page 0 for none: masked)
+    const uint32_t in_page = (t0 + 16 * sixteen) & ((1 << a.c.page_log2) - 1);
+    const uint64_t code = (uint64_t)(uint32_t)(page < 0 ? 0 : page) * page_bytes + in_page * (D / 2);
+    const uint64_t scale = code / (B / 2);
+    load_words(kc + code, x.k);
+    load_words(vc + code, x.v);
+    x.ks = *reinterpret_cast<const uint32_t*>(ks + scale);
+    x.vs = *reinterpret_cast<const uint32_t*>(vs + scale);
+  };
+  // Word j of a fetched piece, dequantized to its place.
+  uint32_t k_to[W], v_to[W];
 #pragma unroll
-      for (int j = 0; j < QK; ++j) {
-        float x[16];
-        load_q16(q + 16 * j, a.c.rht, a.c.signs, x);
+  for (int j = 0; j < W; ++j) {
+    k_to[j] = many_k_at<D>(st_row, st_seg * W + j);
+    v_to[j] = many_v_at<D>(st_row, st_seg * W + j) + 2 * kTile;
+  }
+  auto put = [&](uint32_t w, uint32_t scales, int j, uint32_t at) __attribute__((always_inline)) {
+    Scale<MX> k;
+    block_scale(scales, block_of_word<MX>(j), k);
+    *reinterpret_cast<w4*>(lds + at) = dequant8(w, k);
+  };
+  // What no row sees may hold anything: zeros, so that a masked key meets no
+  // NaN.  held: which sixteens of the tile have a page.
+  auto clean = [&](Raw& x, int t0, int held) __attribute__((always_inline)) {
+    x.ks >>= st_shift;
+    x.vs >>= st_shift;
+    if (t0 + kManyKeys > keys.hi || (t0 < keys.lo && t0 + kManyKeys > a.sinks) || held != 15) {
+      const int t = t0 + st_row;
+      const bool ok = ((held >> (wave * kRowsOfWave / 16)) & 1) && t < keys.hi && (t >= keys.lo || t < a.sinks);
+      x.ks = ok ? x.ks : 0u;
+      x.vs = ok ? x.vs : 0u;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(x[e]));
+      for (int j = 0; j < W; ++j) {
+        x.k[j] = ok ? x.k[j] : 0u;
+        x.v[j] = ok ? x.v[j] : 0u;
       }
-      row_power(mx, down, up);
     }
-    rs = score_scale<MX>(a, up);
+  };
+
+  f32x16 o[DT];
+  float top = -__builtin_inff(), l = 0.0f;  // l: this lane's keys only
+#pragma unroll
+  for (int j = 0; j < DT; ++j) o[j] = f32x16{};
+
+  if (begin < end) {
+    Raw cur, nxt;
+    int pages = pages_at(begin), pages1 = pages_at(begin + 1), pages2 = pages_at(begin + 2);
+
+    // the lane's row: fragments of q (columns 16 j + 8 half + 0..7), score
+    // scale, visible range
+    w4 raw_q[QK];
+    const int my_row = works ? (w0 + qrow < r1 ? w0 + qrow : r1 - 1) : r0;
+    const int my_token = my_row / a.group;
+    {
+      const int head = h * a.group + my_row - my_token * a.group;
+      const uint16_t* q = a.q + (s.first + my_token) * a.q_token + head * a.q_head + 8 * half;
+#pragma unroll
+      for (int j = 0; j < QK; ++j) raw_q[j] = *reinterpret_cast<const w4*>(q + 16 * j);
+    }
+    auto held_of = [&](int p) __attribute__((always_inline)) { return (int)(__ballot(p >= 0) & 15u); };
+    int held = held_of(pages), held_next = held_of(pages1);
+    fetch(begin, pages, cur);
+    fetch(begin + 1, pages1, nxt);
+    x8 qf[QK], ql[LO ? QK : 1];
+    const float sign = score_sign<MX>(a);
+    float down = 1.0f, up = 1.0f;
+    if constexpr (!MX) {
+      // the largest magnitude before the rotation, which multiplies it by 4
+      // at most: FP16 has room for that
+      uint32_t mx = 0;
+#pragma unroll
+      for (int j = 0; j < QK; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = raw_q[j][e], lo = w << 16 & 0x7FFF0000u, hi = w & 0x7FFF0000u;
+          mx = mx > lo ? mx : lo;
+          mx = mx > hi ? mx : hi;
+        }
+      const float m = __uint_as_float(mx);
+      row_power(fmaxf(m, __shfl_xor(m, 32)), down, up);
+    }
+    const float rs = score_scale<MX>(a, up);
+    down *= sign;
 #pragma unroll
     for (int j = 0; j < QK; ++j) {
-      float x[16];
-      load_q16(q + 16 * j, a.c.rht, a.c.signs, x);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = bf16_lo(raw_q[j][e]);
+        x[2 * e + 1] = bf16_hi(raw_q[j][e]);
+      }
+      if (a.c.rht) {  // stages 1, 2, 4 in the lane, 8 with the other half's
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[e] = __uint_as_float(__float_as_uint(x[e]) ^ (((a.c.signs >> (8 * half + e)) & 1u) << 31));
+#pragma unroll
+        for (int st = 1; st < 8; st <<= 1)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (e & st) continue;
+            const float p = x[e], q = x[e + st];
+            x[e] = p + q;
+            x[e + st] = p - q;
+          }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float other = __shfl_xor(x[e], 32);
+          x[e] = (half ? other - x[e] : x[e] + other) * 0.25f;
+        }
+      }
       w4 w, y;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float u = (half ? x[8 + 2 * e] : x[2 * e]) * sign * down;
-        const float v = (half ? x[9 + 2 * e] : x[2 * e + 1]) * sign * down;
+        const float u = x[2 * e] * down, v = x[2 * e + 1] * down;
         w[e] = pack2<MX>(u, v);
         if constexpr (LO)
           y[e] = pack2<MX>(u - __uint_as_float(w[e] << 16), v - __uint_as_float(w[e] & 0xFFFF0000u));
       }
+      // one wave to a SIMD: accumulation registers hold q, which only matrix
+      // instructions read
+      if constexpr (kWaves == 4) asm volatile("" : "+a"(w));
       qf[j] = as8<MX>(w);
       if constexpr (LO) ql[j] = as8<MX>(y);
     }
-  }
-  const int64_t p = s.pos + qi;
-  const int hi_row = (int)(p + 1 < 0 ? 0 : (p + 1 < s.kv ? p + 1 : s.kv));
-  const int lo_row = a.window > 0 && p + 1 > a.window ? (int)(p + 1 - a.window < s.kv ? p + 1 - a.window : s.kv) : 0;
-  // keys that every row of this wave sees, and keys that any row sees
-  const int64_t p0 = s.pos + w0 / a.group, p1 = s.pos + (w1 - 1) / a.group;
-  const int all_hi = (int)(p0 + 1 < 0 ? 0 : (p0 + 1 < s.kv ? p0 + 1 : s.kv));
-  const int64_t all_lo = a.window > 0 ? p1 + 1 - a.window : 0;
-  const int any_hi = works ? (int)(p1 + 1 < 0 ? 0 : (p1 + 1 < s.kv ? p1 + 1 : s.kv)) : 0;
-  const int64_t any_lo = a.window > 0 ? p0 + 1 - a.window : 0;
+    const int64_t p = s.pos + my_token;
+    const int hi_row = (int)(p + 1 < 0 ? 0 : (p + 1 < s.kv ? p + 1 : s.kv));
+    const int lo_row = a.window > 0 && p + 1 > a.window ? (int)(p + 1 - a.window < s.kv ? p + 1 - a.window : s.kv) : 0;
+    // keys that every row of this wave sees
+    const int64_t p0 = s.pos + (works ? w0 : r0) / a.group, p1 = s.pos + ((works ? w1 : r1) - 1) / a.group;
+    const int all_hi = (int)(p0 + 1 < 0 ? 0 : (p0 + 1 < s.kv ? p0 + 1 : s.kv));
+    const int64_t all_lo = a.window > 0 ? p1 + 1 - a.window : 0;
 
-  f32x16 o[DT];
+    // the lane's places: K's row, and in a transposing read of V (lane group:
+    // half, column half) one of four tokens and four columns
+    const int tr_lane = lane & 15, tr_row = 4 * half + (tr_lane >> 2);
+    const int tr_piece = 2 * ((lane >> 4) & 1) + ((tr_lane & 3) >> 1), tr_in = (tr_lane & 1) * 8;
+    uint32_t k_at[QK], v_at[DT];
 #pragma unroll
-  for (int j = 0; j < DT; ++j) o[j] = f32x16{};
-  float top = -__builtin_inff(), l = 0.0f;  // l: this lane's keys only
-
-  // Staging: threads 0..255 take K, 256..511 V: four threads to a row, a
-  // quarter (D / 4 codes) each.
-  const bool is_v = threadIdx.x >= 256;
-  const int st_row = (threadIdx.x & 255) >> 2, st_seg = threadIdx.x & 3;
-  const uint8_t* st_codes = is_v ? a.c.v_codes : a.c.k_codes;
-  const uint8_t* st_scales = is_v ? a.c.v_scales : a.c.k_scales;
-  uint32_t raw[W], raw_s = 0;
-  auto fetch = [&](int t0) {
-    const int t = t0 + st_row;
-    int page = -1;
-    if (t < keys.hi && (t >= keys.lo || t < a.sinks)) {
-      page = a.b.page_table[seq * a.b.table_ld + (t >> a.c.page_log2)];
-      if (page < 0 || page >= a.c.pages) page = -1;
-    }
+    for (int j = 0; j < QK; ++j) k_at[j] = many_k_at<D>(qrow, 2 * j + half);
 #pragma unroll
-    for (int j = 0; j < W; ++j) raw[j] = 0;
-    raw_s = 0;
-    if (page >= 0) {  // the rest stays zero: a masked key meets no NaN
-      const int64_t row = row_of(a, page, h, t);
-      load_words(st_codes + row * (D / 2) + st_seg * (D / 8), raw);
-      raw_s = load_scales<MX, D>(st_scales + row * (D / B), st_seg);
-    }
-  };
-  auto stage = [&](int buf) {
-    uint8_t* to = lds + buf * 2 * kTile + (is_v ? kTile : 0);
+    for (int j = 0; j < DT; ++j) v_at[j] = many_v_at<D>(tr_row, 4 * j + tr_piece) + tr_in + 2 * kTile;
+    // K's fragment j of a sub-tile (constant offsets: `at` is a constant)
+    auto read_k = [&](int j, int at) __attribute__((always_inline)) { return as8<MX>(*reinterpret_cast<const w4*>(lds + k_at[j] + at)); };
+    // V's fragment k: 16 keys b = k / DT, {4 half + i, 8 + 4 half + i} of
+    // them, columns 32 (k % DT)
+    auto read_v = [&](int k, int at) __attribute__((always_inline)) {
+      const uint8_t* p = lds + v_at[k % DT] + (at + 16 * (k / DT) * (2 * D));
+      const w2 x = read_tr16(p), y = read_tr16(p + 8 * (2 * D));
+      return as8<MX>(w4{x.x, x.y, y.x, y.y});
+    };
+    auto mask = [&](f32x16& sc, int t0, int held2) __attribute__((always_inline)) {
+      int th = t0 + 4 * half;
+      asm volatile("" : "+v"(th));  // a branch: most tiles skip this
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      Scale<MX> k;
-      block_scale(raw_s, block_of_word<MX>(j), k);
-      const int pc = st_seg * W + j;
-      *reinterpret_cast<w4*>(to + (is_v ? many_v_at<D>(st_row, pc) : many_k_at<D>(st_row, pc))) =
-          dequant8(raw[j], k);
-    }
-  };
-  // rows of a transposing read: lane group (half, column half), four tokens
-  const int tr_lane = lane & 15, tr_dh = (lane >> 4) & 1;
-  const int tr_row = 4 * half + (tr_lane >> 2);
-  const int tr_piece = 2 * tr_dh + ((tr_lane & 3) >> 1), tr_in = (tr_lane & 1) * 8;
-
-  // tiles without a page (the sequence gave it back) hold zeros, which are
-  // not keys: their scores are masked by the page table in the masked path
-  if (begin < end) {
-    fetch(keys.base(begin));
-    stage(0);
-  }
-  for (int u = begin; u < end; ++u) {
-    const int t0 = keys.base(u), buf = (u - begin) & 1;
-    if (u + 1 < end) fetch(keys.base(u + 1));
-    __syncthreads();
-    const uint8_t* kt = lds + buf * 2 * kTile;
-    const uint8_t* vt = kt + kTile;
-    const bool skip = t0 >= any_hi || (t0 + kManyKeys <= any_lo && t0 >= a.sinks);
-    if (!skip) {
-      f32x16 sc[2];
+      for (int b = 0; b < 4; ++b) {
+        const bool has = (held2 >> (b >> 1)) & 1;  // sixteen keys of one page
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        sc[c] = f32x16{};
-#pragma unroll
-        for (int j = 0; j < QK; ++j) {
-          const x8 kf = as8<MX>(*reinterpret_cast<const w4*>(kt + many_k_at<D>(32 * c + qrow, 2 * j + half)));
-          sc[c] = N::mma(kf, qf[j], sc[c]);
-          if constexpr (LO) sc[c] = N::mma(kf, ql[j], sc[c]);
+        for (int i = 0; i < 4; ++i) {
+          const int t = th + 8 * b + i;
+          const bool seen = has && t < hi_row && (t >= lo_row || t < a.sinks);
+          sc[4 * b + i] = seen ? sc[4 * b + i] : -__builtin_inff();
         }
       }
-      bool pages = true;
-      for (int t = t0; t < t0 + kManyKeys; t += 16)
-        pages = pages && page_of(a, seq, t, keys.hi) >= 0;
-      if (!(t0 + kManyKeys <= all_hi && t0 >= all_lo && pages)) {
+    };
+    // The maximum is raised where a score passes it by 2^8 (rare, as above);
+    // f is what the sums before count for then.
+    auto raise = [&](float peak, float& f) __attribute__((always_inline)) -> int {
+      const float mx = peak * rs;
+      if (!__any(mx > top + 8.0f)) return 0;
+      const float t = fmaxf(top, fmaxf(mx, __shfl_xor(mx, 32)));
+      f = t == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(top - t);
+      top = t;
+      l *= f;
+      return 1;
+    };
+
+    // Half a tile: the exponentials of the scores `sc` (keys t0 .. t0 + 31)
+    // into `p`; the scores of the next half (K at k_off) into `next`; the
+    // output of the half before (probabilities `before`, V at v_off); and the
+    // next tile's K or V (words `w`) into LDS at `to` + `to_off`.  Written out
+    // instruction group by instruction group, and kept so: behind every
+    // matrix instruction the vector work that fits into its time.
+    auto half_tile = [&](f32x16& sc, int t0, int held2, w4 (&p)[2], f32x16& next, int k_off,
+                         const w4 (&before)[2], int v_off, const uint32_t (&w)[W],
+                         uint32_t scales, const uint32_t (&to)[W], int to_off) __attribute__((always_inline)) {
+      constexpr int kSteps = QK;              // = 2 * DT: fragments of K and of V
+      constexpr int E = 16 / kSteps;  // scores of a step
+      x8 vf = read_v(0, v_off);
+      if (!(t0 + 32 <= all_hi && t0 >= all_lo && held2 == 3)) mask(sc, t0, held2);
+      // the first kAhead steps of the output, beside them the scores' maxima
+      constexpr int kAhead = kSteps / 2;
+      float f = 1.0f, odd = 0.0f, peak = sc[0];
+      x8 kf;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+      for (int k = 0; k < kAhead; ++k) {
+        x8 vn = read_v(k + 1, v_off);
+        if (k + 1 == kAhead) kf = read_k(0, k_off);
+        __builtin_amdgcn_sched_barrier(0);
+        o[k % DT] = N::mma(vf, as8<MX>(before[k / DT]), o[k % DT]);
+        constexpr int T = 16 / kAhead;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int tb = t0 + 32 * c + 8 * b;  // eight keys of one page
-            const bool has = page_of(a, seq, tb, keys.hi) >= 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int t = tb + 4 * half + i;
-              const bool seen = has && t < hi_row && (t >= lo_row || t < a.sinks);
-              sc[c][4 * b + i] = seen ? sc[c][4 * b + i] : -__builtin_inff();
-            }
-          }
+        for (int i = k * T; i < (k + 1) * T; ++i) peak = fmaxf(peak, sc[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        vf = vn;
       }
-      float mx = sc[0][0];
+      int raised = __builtin_amdgcn_readfirstlane(raise(peak, f));
+      asm volatile("" : "+s"(raised));  // one copy of what follows, not one for each case
+      asm volatile("" : "+v"(top));
+      const float sub = top == -__builtin_inff() ? 0.0f : top;
+      next = f32x16{};
+      // the n-th of a step's M slots of vector work
+      auto vector_work = [&](int k, int n, int M) __attribute__((always_inline)) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+        for (int e = k * E + n * E / M; e < k * E + (n + 1) * E / M; ++e) {
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[e], rs, -sub));
+          if (e % 2 == 0) {
+            odd = x;
+          } else {
+            const uint32_t both = pack2<MX>(odd, x);
+            p[e / 8][(e % 8) / 2] = both;
+            l = add_pair<MX>(both, l);
+          }
+        }
+        if (n == M - 1 && k % (kSteps / W) == kSteps / W - 1)
+          put(w[k / (kSteps / W)], scales, k / (kSteps / W), to[k / (kSteps / W)] + to_off);
+      };
+      // every step the scores' next fragment, every other step the output's
 #pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[c][i]);
-      mx *= rs;
-      if (__any(mx > top + 8.0f)) {  // as above: the maximum is raised rarely
-        const float t = fmaxf(top, fmaxf(mx, __shfl_xor(mx, 32)));
-        const float f = t == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(top - t);
-        top = t;
-        l *= f;
+      for (int k = 0; k < kSteps; ++k) {
+        const int kv = kAhead + k / 2;
+        const bool out = k % 2 == 1;
+        const int M = (LO ? 2 : 1) + (out ? 1 : 0);
+        x8 kn = kf, vn = vf;
+        if (k + 1 < kSteps) kn = read_k(k + 1, k_off);
+        if (out && kv + 1 < kSteps) vn = read_v(kv + 1, v_off);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < M; ++n) {
+          if (n == 0) next = N::mma(kf, qf[k], next);
+          else if (LO && n == 1) next = N::mma(kf, ql[LO ? k : 0], next);
+          else o[kv % DT] = N::mma(vf, as8<MX>(before[kv / DT]), o[kv % DT]);
+          vector_work(k, n, M);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        kf = kn;
+        if (out) vf = vn;
+      }
+      // the exponentials stay in this half (nothing here uses them: they would
+      // be sunk to the next one's output)
+      asm volatile("" : "+v"(p[0]));
+      asm volatile("" : "+v"(p[1]));
+      if (raised) {
 #pragma unroll
         for (int j = 0; j < DT; ++j) o[j] *= f;
       }
-      const float sub = top == -__builtin_inff() ? 0.0f : top;
+    };
+
+    // The first tile, and zeros where the output step before it would read
+    clean(cur, keys.base(begin), held);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {  // 16 keys: t0 + 32 c + 16 b + {4 half + i, 8 + 4 half + i}
-          w4 w;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[c][8 * b + 2 * i], rs, -sub));
-            const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[c][8 * b + 2 * i + 1], rs, -sub));
-            w[i] = pack2<MX>(x, y);
-            if constexpr (MX) {
-              l += __uint_as_float(w[i] << 16);
-              l += __uint_as_float(w[i] & 0xFFFF0000u);
-            } else {
-              l += x;
-              l += y;
-            }
-          }
-          const x8 pf = as8<MX>(w);
-          const int tr = 32 * c + 16 * b + tr_row;
-#pragma unroll
-          for (int j = 0; j < DT; ++j) {
-            const w2 x = read_tr16(vt + many_v_at<D>(tr, 4 * j + tr_piece) + tr_in);
-            const w2 y = read_tr16(vt + many_v_at<D>(tr + 8, 4 * j + tr_piece) + tr_in);
-            o[j] = N::mma(as8<MX>(w4{x.x, x.y, y.x, y.y}), pf, o[j]);
-          }
-        }
-      }
+    for (int j = 0; j < W; ++j) {
+      put(cur.k[j], cur.ks, j, k_to[j]);
+      put(cur.v[j], cur.vs, j, v_to[j]);
     }
-    if (u + 1 < end) stage(buf ^ 1);
+    {
+      uint8_t* z = lds + 3 * kTile;
+#pragma unroll
+      for (int i = 0; i < kTile / (16 * kManyThreads); ++i)
+        reinterpret_cast<w4*>(z)[threadIdx.x + i * kManyThreads] = w4{};
+    }
+    cur = nxt;
+    __syncthreads();
+    f32x16 sa = {}, sb;
+    w4 pa[2], pb[2] = {};
+#pragma unroll
+    for (int j = 0; j < QK; ++j) {
+      const x8 kf = read_k(j, 0);
+      sa = N::mma(kf, qf[j], sa);
+      if constexpr (LO) sa = N::mma(kf, ql[j], sa);
+    }
+    constexpr int kSub = 32 * 2 * D;  // bytes from a sub-tile to the next
+    // Tile u in buffer `buf` (a constant).
+    auto tile = [&](int u, int buf) __attribute__((always_inline)) {
+      const int t0 = keys.base(u), other = buf ^ 1;
+      const int held_after = held_of(pages2);
+      fetch(u + 2, pages2, nxt);
+      pages2 = pages_at(u + 3);
+      clean(cur, keys.base(u + 1 < last ? u + 1 : last), held_next);
+      // the next tile's K goes where the tile before had its own, its V
+      // (after the barrier) likewise
+      half_tile(sa, t0, held & 3, pa, sb, buf * kTile + kSub, pb, other * kTile + kSub, cur.k, cur.ks,
+                k_to, other * kTile);
+      __syncthreads();
+      half_tile(sb, t0 + 32, held >> 2, pb, sa, other * kTile, pa, buf * kTile, cur.v, cur.vs, v_to,
+                other * kTile);
+      cur = nxt;
+      held = held_next;
+      held_next = held_after;
+    };
+    int u = begin;
+    for (; u + 1 < end; u += 2) {
+      tile(u, 0);
+      tile(u + 1, 1);
+    }
+    int last_buf = 1;
+    if (u < end) {
+      tile(u, 0);
+      last_buf = 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 2 * DT; ++k) {
+      o[k % DT] = N::mma(read_v(k, last_buf * kTile + kSub), as8<MX>(pb[k / DT]), o[k % DT]);
+    }
   }
 
-  if (!works || w0 + qrow >= r1) return;
-  l += __shfl_xor(l, 32);  // both halves of a row are here or neither
+  const int r = w0 + qrow;
+  l += __shfl_xor(l, 32);
+  const int qi = r / a.group, head = h * a.group + r - qi * a.group;
   const int64_t token = s.first + qi;
-  if (a.splits == 1) {
-    const float f = out_factor<MX>(a, l);
-    const int64_t at = token * a.out_token + head * a.out_head;
+  const int64_t slot = ((int64_t)split * a.b.tokens + token) * a.q_heads + head;
+  const float f = a.splits == 1 ? out_factor<MX>(a, l) : 1.0f;
+  const int64_t at = token * a.out_token + head * a.out_head;
 #pragma unroll
-    for (int j = 0; j < DT; ++j) {
+  for (int j = 0; j < DT; ++j) {
+    if (a.splits == 1) {
       o[j] *= f;
       if (a.c.rht) rotate_back32(o[j], half, a.c.signs);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int d = 32 * j + 8 * b + 4 * half;
-        if (a.out_f32)
-          *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + d) =
-              f32x4{o[j][4 * b], o[j][4 * b + 1], o[j][4 * b + 2], o[j][4 * b + 3]};
-        else
-          *reinterpret_cast<w2*>(static_cast<uint16_t*>(a.out) + at + d) =
-              w2{bf16_pair(o[j][4 * b], o[j][4 * b + 1]), bf16_pair(o[j][4 * b + 2], o[j][4 * b + 3])};
-      }
     }
-    if (a.lse && half == 0) a.lse[token * a.q_heads + head] = row_lse(top, l);
-  } else {
-    const int64_t at = ((int64_t)split * a.b.tokens + token) * a.q_heads + head;
-    if (half == 0) a.part_ml[at] = make_float2(top, l);
-    if (l > 0.0f) {
+    if (r >= r1) continue;
 #pragma unroll
-      for (int j = 0; j < DT; ++j)
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          *reinterpret_cast<f32x4*>(a.part + at * D + 32 * j + 8 * b + 4 * half) =
-              f32x4{o[j][4 * b], o[j][4 * b + 1], o[j][4 * b + 2], o[j][4 * b + 3]};
+    for (int b = 0; b < 4; ++b) {
+      const int d = 32 * j + 8 * b + 4 * half;
+      const f32x4 v = {o[j][4 * b], o[j][4 * b + 1], o[j][4 * b + 2], o[j][4 * b + 3]};
+      if (a.splits > 1) *reinterpret_cast<f32x4*>(a.part + slot * D + d) = v;
+      else if (a.out_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + d) = v;
+      else
+        *reinterpret_cast<w2*>(static_cast<uint16_t*>(a.out) + at + d) = w2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
     }
+  }
+  if (r < r1 && half == 0) {
+    if (a.splits > 1) a.part_ml[slot] = make_float2(top, l);
+    else if (a.lse) a.lse[token * a.q_heads + head] = row_lse(top, l);
   }
 }
 
@@ -1357,7 +1522,7 @@ hipError_t launch_d(const Args& a, const KvAttentionPlan& p, hipStream_t s) {
   if (!p.prompt)
     return p.rows == 16 ? launch_few<MX, LO, D, 1>(a, s)
                         : launch_few<MX, LO, D, D <= 128 ? 2 : 1>(a, s);
-  kv_many_kernel<MX, LO, D><<<(unsigned)p.groups, kManyThreads, 0, s>>>(a);
+  kv_many_kernel<MX, LO, D><<<(unsigned)p.groups, 64 * many_waves(D), 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 grid((unsigned)a.b.max_q * (unsigned)a.q_heads, (unsigned)a.b.batch);
@@ -1382,7 +1547,7 @@ KvAttentionPlan fp4_plan_kv_attention(const KvCacheArgs& c, const KvBatchArgs& b
   const int64_t rows = (int64_t)b.max_q * (q_heads / c.heads);
   p.prompt = rows > 64;
   // 32 rows of 256 columns would leave a compute unit one workgroup
-  p.rows = p.prompt ? kManyRows : (rows > 16 && c.dim <= 128 ? 32 : 16);
+  p.rows = p.prompt ? many_rows(c.dim) : (rows > 16 && c.dim <= 128 ? 32 : 16);
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
   const int64_t seen = max_keys(b.max_kv, window, sinks, b.max_q);
   const int64_t segments = (int64_t)b.batch * c.heads * p.row_tiles;
