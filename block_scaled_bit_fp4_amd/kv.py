@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -61,26 +62,17 @@ class KVBatch(NamedTuple):
     max_kv: int = 0
 
 
-class _Cache(ctypes.Structure):
-    _fields_ = [("format", ctypes.c_int32), ("layers", ctypes.c_int32), ("heads", ctypes.c_int32),
-                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("rht", ctypes.c_int32), ("rht_seed", ctypes.c_uint64), ("pages", ctypes.c_int64),
-                ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
-                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
-
-
-class _Batch(ctypes.Structure):
-    _fields_ = [("page_table", ctypes.c_void_p), ("table_ld", ctypes.c_int64),
-                ("kv_lens", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
-                ("batch", ctypes.c_int32), ("columns", ctypes.c_int32),
-                ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32)]
+# fp4_kv_cache and fp4_kv_batch of include/fp4.h, packed per call (a quarter of
+# the time of ctypes structures: a single token's call is bound by the host)
+_CACHE = struct.Struct("@iiiiiiQqPPPPPP")
+_BATCH = struct.Struct("@PqPPiiii")
+_FORMAT = {f: (fp4.FORMATS[f], fp4.BLOCK[f]) for f in KV_FORMATS}
 
 
 def bind(L):
     """Argument types of the cache's entry points."""
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-    C, B = ctypes.POINTER(_Cache), ctypes.POINTER(_Batch)
+    C = B = ctypes.c_char_p  # the packed structures
     L.fp4_kv_append.argtypes = [C, i32, B, vp, i64, i64, vp, i64, i64, i32, i64, vp]
     L.fp4_kv_gather.argtypes = [C, i32, B, vp, vp, i64, i64, i32, i64, vp]
     L.fp4_kv_attention_workspace_bytes.argtypes = [C, B, i32, i64, i32, i32]
@@ -129,62 +121,88 @@ def _need(ok, msg):
 
 
 def _ints(t, name, dims=1, device=None):
-    if not (torch.is_tensor(t) and t.dtype == torch.int32 and t.dim() == dims and t.is_cuda
-            and (t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1)):
+    """Checks an int32 tensor on the device of that index (None: any)."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if not (dev >= 0 and t.dtype is torch.int32 and t.dim() == dims
+            and (t.is_contiguous() or t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1)):
         raise ValueError("%s must be a %d-D int32 device tensor with dense rows" % (name, dims))
-    if device is not None and t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
-    return t
+    if device is not None and dev != device:
+        raise ValueError("%s must be on device %d" % (name, device))
 
 
-def _cache(c: KVCache) -> _Cache:
-    kc = c.k_codes
-    if c.fmt not in KV_FORMATS:
+def _pack(layout, *values):
+    try:
+        return layout.pack(*values)
+    except struct.error as e:
+        raise ValueError("a size is out of range: %s" % e) from None
+
+
+def _cache(c: KVCache):
+    """(the packed cache, its pages, heads and head_dim, its device's index)"""
+    kc, ks, vc, vs, kf, vf, fmt, rht, seed = c
+    if fmt not in _FORMAT:
         raise ValueError("a cache is held in one of %s" % (KV_FORMATS,))
-    if kc.dim() != 5:
+    code, block = _FORMAT[fmt]
+    shape = kc.shape
+    if len(shape) != 5:
         raise ValueError("codes are [layers, pages, heads, page_size, head_dim / 2]")
-    layers, pages, heads, page, half = kc.shape
-    scales = (layers, pages, heads, page, 2 * half // fp4.BLOCK[c.fmt])
-    if c.v_codes.shape != kc.shape or c.k_scales.shape != scales or c.v_scales.shape != scales:
+    layers, pages, heads, page, half = shape
+    scales = (layers, pages, heads, page, 2 * half // block)
+    if vc.shape != shape or ks.shape != scales or vs.shape != scales:
         raise ValueError("the cache's arrays do not agree in shape")
-    dev = kc.device
-    for t in (kc, c.k_scales, c.v_codes, c.v_scales):
-        if t.dtype != torch.uint8 or not t.is_contiguous() or not t.is_cuda or t.device != dev:
+    dev = kc.get_device()
+    for t in (kc, ks, vc, vs):
+        if t.dtype is not torch.uint8 or not t.is_contiguous() or dev < 0 or t.get_device() != dev:
             raise ValueError("the cache's arrays are dense uint8 tensors on one device")
-    ks = vs = None
-    if c.fmt == "nvfp4":
-        for t in (c.k_scale, c.v_scale):
-            if t is not None and not (t.dtype == torch.float32 and t.numel() == layers
-                                      and t.is_contiguous() and t.device == dev):
+    kp = vp = 0
+    if fmt == "nvfp4":
+        for t in (kf, vf):
+            if t is not None and not (t.dtype is torch.float32 and t.numel() == layers
+                                      and t.is_contiguous() and t.get_device() == dev):
                 raise ValueError("k_scale and v_scale are float32 [layers] on the cache's device")
-        ks, vs = fp4._ptr(c.k_scale), fp4._ptr(c.v_scale)
-    return _Cache(fp4.FORMATS[c.fmt], layers, heads, 2 * half, page, int(bool(c.rht)),
-                  int(c.rht_seed) & (2**64 - 1), pages, kc.data_ptr(), c.k_scales.data_ptr(),
-                  c.v_codes.data_ptr(), c.v_scales.data_ptr(), ks, vs)
+        kp, vp = kf.data_ptr() if kf is not None else 0, vf.data_ptr() if vf is not None else 0
+    return _pack(_CACHE, code, layers, heads, 2 * half, page, bool(rht), seed & (2**64 - 1), pages,
+                 kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), kp, vp), \
+        pages, heads, 2 * half, dev
 
 
-def _batch(b: KVBatch, device) -> _Batch:
-    t, n = b.page_table, b.kv_lens
-    _ints(t, "page_table", 2, device)
-    _ints(n, "kv_lens", 1, device)
-    _ints(b.cu_q, "cu_q", 1, device)
-    size = t.shape[0]
-    if n.shape[0] != size or b.cu_q.shape[0] != size + 1:
+def _batch(b: KVBatch, device):
+    table, lens, cu_q, max_q, max_kv = b
+    _ints(table, "page_table", 2, device)
+    _ints(lens, "kv_lens", 1, device)
+    _ints(cu_q, "cu_q", 1, device)
+    size, columns = table.shape
+    if lens.numel() != size or cu_q.numel() != size + 1:
         raise ValueError("page_table, kv_lens and cu_q are of different batches")
-    return _Batch(t.data_ptr(), t.stride(0) if size > 1 else max(t.shape[1], 1), n.data_ptr(),
-                  b.cu_q.data_ptr(), size, t.shape[1], int(b.max_q), int(b.max_kv))
+    return _pack(_BATCH, table.data_ptr(), table.stride(0) if size > 1 else max(columns, 1),
+                 lens.data_ptr(), cu_q.data_ptr(), size, columns, max_q, max_kv)
 
 
 def _rows(t, name, heads, dim, dtypes, device):
-    """A [tokens, heads, head_dim] tensor with a dense last dimension; its
-    strides (of a dimension of one, none that matter)."""
-    if not torch.is_tensor(t) or t.dim() != 3 or t.shape[2] != dim or (heads and t.shape[1] != heads):
+    """The strides of a [tokens, heads, head_dim] tensor with a dense last
+    dimension (of a dimension of one, none that matter), its tokens and heads."""
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    if len(shape) != 3 or shape[2] != dim or (heads and shape[1] != heads):
         raise ValueError("%s must be [tokens, %s, %d]" % (name, heads or "heads", dim))
     if t.dtype not in dtypes:
         raise TypeError("%s has type %s" % (name, t.dtype))
-    if t.device != device or t.stride(2) != 1:
-        raise ValueError("%s must be on %s with a dense last dimension" % (name, device))
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+    st = t.stride()
+    if t.get_device() != device or st[2] != 1:
+        raise ValueError("%s must be on device %d with a dense last dimension" % (name, device))
+    return (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0), shape[0], shape[1]
+
+
+def _empty(stream, shape, dtype, device, what):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with fp4._Alloc(stream) as al:
+        return al.empty(shape, dtype, device, what)
+
+
+def _stream(stream):
+    if stream is None:  # the current device's current stream, without an object for it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return fp4._stream(stream)
 
 
 def _raise(st, name):
@@ -197,15 +215,14 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, batch: KVBatch, 
     """Quantize the new tokens' keys and values ([tokens, heads, head_dim], BF16
     or FP32, any strides that keep rows 16-byte aligned: views of a fused
     projection, say) into their places in a layer."""
-    c = _cache(cache)
-    dev = cache.k_codes.device
+    c, _, heads, dim, dev = _cache(cache)
     b = _batch(batch, dev)
-    ks = _rows(k, "k", c.heads, c.head_dim, fp4.DTYPES, dev)
-    vs = _rows(v, "v", c.heads, c.head_dim, fp4.DTYPES, dev)
-    _need(k.shape == v.shape and k.dtype == v.dtype, "k and v must agree in shape and type")
-    _raise(fp4.load().fp4_kv_append(c, layer, b, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
-                                    vs[1], fp4.DTYPES[k.dtype], k.shape[0], fp4._stream(stream)),
-           "fp4_kv_append")
+    k0, k1, tokens, _ = _rows(k, "k", heads, dim, fp4.DTYPES, dev)
+    v0, v1, v_tokens, _ = _rows(v, "v", heads, dim, fp4.DTYPES, dev)
+    dtype = k.dtype
+    _need(tokens == v_tokens and dtype is v.dtype, "k and v must agree in shape and type")
+    _raise(fp4.load().fp4_kv_append(c, layer, b, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1,
+                                    fp4.DTYPES[dtype], tokens, _stream(stream)), "fp4_kv_append")
 
 
 def kv_gather(cache: KVCache, batch: KVBatch, tokens: int, layer: int = 0,
@@ -214,29 +231,27 @@ def kv_gather(cache: KVCache, batch: KVBatch, tokens: int, layer: int = 0,
     (k, v) [tokens, heads, head_dim].  Tokens that the cache does not hold read
     as zeros; rows of no sequence are left as they are.  ``out``: a pair of
     tensors of equal strides to write."""
-    c = _cache(cache)
-    dev = cache.k_codes.device
+    c, _, heads, dim, dev = _cache(cache)
     b = _batch(batch, dev)
     if out is None:
-        with fp4._Alloc(stream) as al:
-            shape = (tokens, c.heads, c.head_dim)
-            out = (al.empty(shape, out_dtype, dev, "k"), al.empty(shape, out_dtype, dev, "v"))
+        shape, device = (tokens, heads, dim), cache.k_codes.device
+        out = (_empty(stream, shape, out_dtype, device, "k"),
+               _empty(stream, shape, out_dtype, device, "v"))
     k, v = out
-    s = _rows(k, "out[0]", c.heads, c.head_dim, fp4.DTYPES, dev)
-    _need(s == _rows(v, "out[1]", c.heads, c.head_dim, fp4.DTYPES, dev) and k.dtype == v.dtype
-          and k.shape == v.shape and k.shape[0] == tokens,
-          "the outputs must agree in shape, type and strides")
+    s = _rows(k, "out[0]", heads, dim, fp4.DTYPES, dev)
+    dtype = k.dtype
+    _need(s == _rows(v, "out[1]", heads, dim, fp4.DTYPES, dev) and dtype is v.dtype
+          and s[2] == tokens, "the outputs must agree in shape, type and strides")
     _raise(fp4.load().fp4_kv_gather(c, layer, b, k.data_ptr(), v.data_ptr(), s[0], s[1],
-                                    fp4.DTYPES[k.dtype], tokens, fp4._stream(stream)),
-           "fp4_kv_gather")
+                                    fp4.DTYPES[dtype], tokens, _stream(stream)), "fp4_kv_gather")
     return k, v
 
 
 def kv_attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int, tokens: int,
                                  window: int = 0, sinks: int = 0) -> int:
     """Bytes of the workspace that ``kv_attention`` needs (0: none)."""
-    c = _cache(cache)
-    b = _batch(batch, cache.k_codes.device)
+    c, _, _, _, dev = _cache(cache)
+    b = _batch(batch, dev)
     return int(fp4.load().fp4_kv_attention_workspace_bytes(c, b, q_heads, tokens, window, sinks))
 
 
@@ -251,31 +266,27 @@ def kv_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, layer: int = 0
     itself included, and the first ``sinks``.  ``lse``: a dense float32 [tokens,
     q_heads] tensor that takes the logarithm of each row's sum of exponentials.
     Rows of no sequence are not written."""
-    c = _cache(cache)
-    dev = cache.k_codes.device
+    c, _, _, dim, dev = _cache(cache)
     b = _batch(batch, dev)
-    qs = _rows(q, "q", 0, c.head_dim, (torch.bfloat16,), dev)
-    tokens, q_heads = q.shape[0], q.shape[1]
+    q0, q1, tokens, q_heads = _rows(q, "q", 0, dim, (torch.bfloat16,), dev)
+    if out is None:
+        out = _empty(stream, (tokens, q_heads, dim), out_dtype, q.device, "out")
+    o0, o1, out_tokens, _ = _rows(out, "out", q_heads, dim, fp4.DTYPES, dev)
+    _need(out_tokens == tokens, "out must have q's shape")
+    if lse is not None:
+        _need(lse.dtype is torch.float32 and lse.shape == (tokens, q_heads)
+              and lse.is_contiguous() and lse.get_device() == dev,
+              "lse must be a dense float32 [tokens, q_heads] tensor on the cache's device")
     L = fp4.load()
-    with fp4._Alloc(stream) as al:
-        if out is None:
-            out = al.empty((tokens, q_heads, c.head_dim), out_dtype, dev, "out")
-        os_ = _rows(out, "out", q_heads, c.head_dim, fp4.DTYPES, dev)
-        _need(out.shape[0] == tokens, "out must have q's shape")
-        if lse is not None:
-            _need(lse.dtype == torch.float32 and lse.shape == (tokens, q_heads)
-                  and lse.is_contiguous() and lse.device == dev,
-                  "lse must be a dense float32 [tokens, q_heads] tensor on the cache's device")
-        if workspace is None:
-            n = L.fp4_kv_attention_workspace_bytes(c, b, q_heads, tokens, window, sinks)
-            if n:
-                workspace = al.empty(n, torch.uint8, dev, "the workspace")
-        st = L.fp4_kv_attention(
-            c, layer, b, q.data_ptr(), qs[0], qs[1], q_heads, tokens,
-            1.0 / math.sqrt(c.head_dim) if scale is None else scale, window, sinks,
-            out.data_ptr(), fp4.DTYPES[out.dtype], os_[0], os_[1], fp4._ptr(lse),
-            fp4._ptr(workspace), fp4._nbytes(workspace), fp4._stream(stream))
-    _raise(st, "fp4_kv_attention")
+    if workspace is None:
+        n = L.fp4_kv_attention_workspace_bytes(c, b, q_heads, tokens, window, sinks)
+        if n:
+            workspace = _empty(stream, n, torch.uint8, q.device, "the workspace")
+    _raise(L.fp4_kv_attention(
+        c, layer, b, q.data_ptr(), q0, q1, q_heads, tokens,
+        1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(),
+        fp4.DTYPES[out.dtype], o0, o1, fp4._ptr(lse), fp4._ptr(workspace), fp4._nbytes(workspace),
+        _stream(stream)), "fp4_kv_attention")
     return out
 
 
@@ -284,9 +295,10 @@ def _tables(table, refs, device, lens=None):
     _ints(refs, "refs", 1, device)
     if lens is not None:
         _ints(lens, "lens", 1, device)
-        _need(lens.shape[0] == table.shape[0], "lens must have a length for every sequence")
-    ld = table.stride(0) if table.shape[0] > 1 else max(table.shape[1], 1)
-    return table.data_ptr(), ld, table.shape[0], table.shape[1]
+        _need(lens.numel() == table.shape[0], "lens must have a length for every sequence")
+    sequences, columns = table.shape
+    ld = table.stride(0) if sequences > 1 else max(columns, 1)
+    return table.data_ptr(), ld, sequences, columns
 
 
 def kv_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor,
@@ -294,8 +306,7 @@ def kv_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor,
     """Page ``dst[i]`` takes page ``src[i]`` in every layer (its first
     ``tokens[i]`` tokens, if given).  int32 device tensors; pages of ``dst`` are
     distinct and none of ``src``; ids out of range are skipped."""
-    c = _cache(cache)
-    dev = cache.k_codes.device
+    c, _, _, _, dev = _cache(cache)
     _ints(src, "src", 1, dev)
     _ints(dst, "dst", 1, dev)
     _need(src.shape == dst.shape, "src and dst must be of one length")
@@ -303,7 +314,7 @@ def kv_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor,
         _ints(tokens, "tokens", 1, dev)
         _need(tokens.shape == src.shape, "tokens must be as long as src")
     _raise(fp4.load().fp4_kv_copy_pages(c, src.data_ptr(), dst.data_ptr(), fp4._ptr(tokens),
-                                        src.shape[0], fp4._stream(stream)), "fp4_kv_copy_pages")
+                                        src.shape[0], _stream(stream)), "fp4_kv_copy_pages")
 
 
 def kv_fork(cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
@@ -315,25 +326,22 @@ def kv_fork(cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor, refs: 
     free page.  Returns a one-element int32 device tensor: the forks that found
     no free page (their children are left empty).  Children are distinct, hold
     no pages and are no parents of the same call."""
-    c = _cache(cache)
-    dev = cache.k_codes.device
+    c, pages, _, _, dev = _cache(cache)
     t = _tables(page_table, refs, dev, lens)
     _ints(parents, "parents", 1, dev)
     _ints(children, "children", 1, dev)
     _need(parents.shape == children.shape, "parents and children must be of one length")
-    _need(refs.shape[0] == c.pages, "refs must have a count for every page")
+    _need(refs.shape[0] == pages, "refs must have a count for every page")
     n = parents.shape[0]
-    with fp4._Alloc(stream) as al:
-        if failed is None:
-            failed = al.empty(1, torch.int32, dev, "failed")
-        _ints(failed, "failed", 1, dev)
-        if workspace is None:
-            workspace = al.empty(16 * max(n, 1), torch.uint8, dev, "the workspace")
-        st = fp4.load().fp4_kv_fork(c, *t, lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
-                                    children.data_ptr(), n, failed.data_ptr(),
-                                    workspace.data_ptr(), fp4._nbytes(workspace),
-                                    fp4._stream(stream))
-    _raise(st, "fp4_kv_fork")
+    device = cache.k_codes.device
+    if failed is None:
+        failed = _empty(stream, 1, torch.int32, device, "failed")
+    _ints(failed, "failed", 1, dev)
+    if workspace is None:
+        workspace = _empty(stream, 16 * max(n, 1), torch.uint8, device, "the workspace")
+    _raise(fp4.load().fp4_kv_fork(c, *t, lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
+                                  children.data_ptr(), n, failed.data_ptr(), workspace.data_ptr(),
+                                  fp4._nbytes(workspace), _stream(stream)), "fp4_kv_fork")
     return failed
 
 
@@ -342,11 +350,12 @@ def kv_free(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, se
     """Give pages of the (distinct) sequences ``seqs`` back: all of them (the
     length becomes 0), or with ``window`` > 0 those that hold none of the last
     ``window`` tokens and none of the first ``sinks``."""
-    t = _tables(page_table, refs, page_table.device, lens)
-    _ints(seqs, "seqs", 1, page_table.device)
+    dev = page_table.get_device()
+    t = _tables(page_table, refs, dev, lens)
+    _ints(seqs, "seqs", 1, dev)
     _raise(fp4.load().fp4_kv_free(*t, lens.data_ptr(), refs.data_ptr(), refs.shape[0], page_size,
                                   seqs.data_ptr(), seqs.shape[0], window, sinks,
-                                  fp4._stream(stream)), "fp4_kv_free")
+                                  _stream(stream)), "fp4_kv_free")
 
 
 def kv_compact(cache: KVCache, page_table: torch.Tensor, refs: torch.Tensor,
@@ -356,22 +365,20 @@ def kv_compact(cache: KVCache, page_table: torch.Tensor, refs: torch.Tensor,
     takes; ``page_table`` and ``refs`` are rewritten.  Returns (place, used):
     each page's new id (-1: it was free) and, in one element, the number of
     pages in use."""
-    c = _cache(cache)
-    dev = cache.k_codes.device
+    c, pages, _, _, dev = _cache(cache)
     t = _tables(page_table, refs, dev)
-    _need(refs.shape[0] == c.pages, "refs must have a count for every page")
-    with fp4._Alloc(stream) as al:
-        if place is None:
-            place = al.empty(c.pages, torch.int32, dev, "place")
-        if used is None:
-            used = al.empty(1, torch.int32, dev, "used")
-        _ints(place, "place", 1, dev)
-        _ints(used, "used", 1, dev)
-        _need(place.shape[0] == c.pages, "place must have an id for every page")
-        if workspace is None:
-            workspace = al.empty(4 * (c.pages + 3), torch.uint8, dev, "the workspace")
-        st = fp4.load().fp4_kv_compact(c, *t, refs.data_ptr(), place.data_ptr(), used.data_ptr(),
-                                       workspace.data_ptr(), fp4._nbytes(workspace),
-                                       fp4._stream(stream))
-    _raise(st, "fp4_kv_compact")
+    _need(refs.shape[0] == pages, "refs must have a count for every page")
+    device = cache.k_codes.device
+    if place is None:
+        place = _empty(stream, pages, torch.int32, device, "place")
+    if used is None:
+        used = _empty(stream, 1, torch.int32, device, "used")
+    _ints(place, "place", 1, dev)
+    _ints(used, "used", 1, dev)
+    _need(place.shape[0] == pages, "place must have an id for every page")
+    if workspace is None:
+        workspace = _empty(stream, 4 * (pages + 3), torch.uint8, device, "the workspace")
+    _raise(fp4.load().fp4_kv_compact(c, *t, refs.data_ptr(), place.data_ptr(), used.data_ptr(),
+                                     workspace.data_ptr(), fp4._nbytes(workspace),
+                                     _stream(stream)), "fp4_kv_compact")
     return place, used
