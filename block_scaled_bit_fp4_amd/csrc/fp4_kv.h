@@ -20,7 +20,7 @@ struct KvCacheArgs {
   const float* k_scale;  // NVFP4: this layer's factor; null for the MX formats
   const float* v_scale;
   int64_t pages;
-  int format, heads, dim;
+  int format, heads, dim, dim_log2;
   int page_log2;
   int rht;
   uint32_t signs;
@@ -75,6 +75,7 @@ struct KvAttentionPlan {
   int rows;       // rows of a workgroup
   int row_tiles;  // of the longest sequence
   int splits;      // many rows: pieces of the keys
+  int pieces;      // few rows: of every row tile's keys; 0: equal runs of all keys
   int64_t groups;  // workgroups
   size_t bytes;    // workspace
 };

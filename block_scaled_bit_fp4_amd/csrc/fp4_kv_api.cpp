@@ -79,6 +79,7 @@ KvCacheArgs layer_of(const fp4_kv_cache* c, int32_t layer) {
   a.format = c->format;
   a.heads = c->heads;
   a.dim = c->head_dim;
+  a.dim_log2 = log2_of(c->head_dim);
   a.page_log2 = log2_of(c->page_size);
   a.rht = c->rht;
   a.signs = c->rht ? fp4_rht_signs(c->rht_seed) : 0u;
@@ -125,11 +126,10 @@ fp4_status check_call(const fp4_kv_cache* c, int32_t layer, const fp4_kv_batch* 
   return check_arrays(c, true);
 }
 
-// Append and gather: one lane per block (16-element group); lanes of the
-// longest sequence in 31 bits.
-fp4_status check_units(const fp4_kv_cache* c, const KvBatchArgs& b, int32_t unit) {
-  return (int64_t)b.max_q * 2 * c->heads * (c->head_dim / unit) > 0x7FFFFFFFll ? FP4_ERR_SHAPE
-                                                                               : FP4_OK;
+// Append and gather number the pieces of the longest sequence's new tokens
+// (of four elements at the least) in 31 bits.
+fp4_status check_units(const fp4_kv_cache* c, const KvBatchArgs& b) {
+  return (int64_t)b.max_q * 2 * c->heads * (c->head_dim / 4) > 0x7FFFFFFFll ? FP4_ERR_SHAPE : FP4_OK;
 }
 
 fp4_status check_attention(const fp4_kv_cache* c, const fp4_kv_batch* b, int32_t q_heads,
@@ -170,7 +170,7 @@ fp4_status fp4_kv_append(const fp4_kv_cache* cache, int32_t layer, const fp4_kv_
   if (in_dtype != FP4_BF16 && in_dtype != FP4_F32) return FP4_ERR_DTYPE;
   KvAppendLaunch q{};
   q.batch = batch_of(cache, batch, tokens);
-  if ((st = check_units(cache, q.batch, block_of(cache))) != FP4_OK) return st;
+  if ((st = check_units(cache, q.batch)) != FP4_OK) return st;
   if (tokens == 0 || q.batch.batch == 0 || q.batch.max_q == 0 || q.batch.columns == 0)
     return FP4_OK;
   if (!k || !v) return FP4_ERR_NULL;
@@ -198,7 +198,7 @@ fp4_status fp4_kv_gather(const fp4_kv_cache* cache, int32_t layer, const fp4_kv_
   if (out_dtype != FP4_BF16 && out_dtype != FP4_F32) return FP4_ERR_DTYPE;
   KvGatherLaunch q{};
   q.batch = batch_of(cache, batch, tokens);
-  if ((st = check_units(cache, q.batch, 16)) != FP4_OK) return st;
+  if ((st = check_units(cache, q.batch)) != FP4_OK) return st;
   if (tokens == 0 || q.batch.batch == 0 || q.batch.max_q == 0) return FP4_OK;
   if (!k_out || !v_out) return FP4_ERR_NULL;
   const int64_t size = out_dtype == FP4_BF16 ? 2 : 4;

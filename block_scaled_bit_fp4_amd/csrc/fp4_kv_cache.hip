@@ -8,22 +8,33 @@
 // one binary32 product, then the inverse RHT.
 //
 // Bound by bytes: 2 * D * element size read and 2 * (D / 2 + D / B) written
-// per token and head (2.28 times less out than in for BF16 NVFP4).  A lane
-// owns one block (16 or 32 elements: 32 to 128 bytes in, 8 or 16 out), so a
-// scale needs no exchange between lanes and every access is 16 bytes wide;
-// consecutive lanes take consecutive blocks of a token, whole 2 * D byte
-// rows of the input.
+// per token and head (2.28 times less out than in for BF16 NVFP4), or the
+// reverse.  Writing takes 32 bytes of a row in a lane, reading back gives 16:
+// consecutive lanes then touch consecutive bytes, and a block or 16-group
+// that lies in two or four lanes is joined by DPP moves.  (A whole block to a
+// lane strides 128 bytes between lanes for FP32.)  A lane has a few pieces in
+// flight, so that the chain length -> page -> data is waited for once, and
+// what is not used again goes past the caches.  51535 tokens of eight FP32
+// heads of 128 columns (MXFP4: 0.48 GB each way) take 105 us to write and 116
+// to read back, 126 and 150 with a lane to a block; without the non-temporal
+// accesses 122 and 143.
 #include "fp4_kv.h"
 #include "fp4_quantize.h"
+
+#include <type_traits>
 
 using namespace fp4kv;
 
 namespace {
 
+// Pieces of a lane, at once.  Writing: 115, 105, 106 us for one, two, four;
+// reading back: 153, 123, 116.  (Single tokens: 3.5, 3.6, 3.9 us of either.)
+constexpr int kAppendPieces = 2, kGatherPieces = 4;
+
 struct AppendArgs {
   KvCacheArgs c;
   KvBatchArgs b;
-  const void* x[2];       // K, V
+  const void* x[2];  // K, V
   int64_t token[2], head[2];
 };
 
@@ -36,12 +47,13 @@ __device__ __forceinline__ int64_t row_of(const KvCacheArgs& c, const KvBatchArg
   return (((int64_t)page * c.heads + h) << c.page_log2) + (pos & ((1 << c.page_log2) - 1));
 }
 
-// Unit u of a sequence's new tokens: token, K or V, head, block of the row.
+// Unit u of a sequence's new tokens: token, K or V, head, piece of the row
+// (1 << log2 pieces).
 struct Unit {
-  int token, part, head, block;
-  __device__ __forceinline__ Unit(uint32_t u, uint32_t heads, uint32_t blocks) {
-    const uint32_t row = u / blocks;
-    block = (int)(u - row * blocks);
+  int token, part, head, piece;
+  __device__ __forceinline__ Unit(uint32_t u, uint32_t heads, int log2) {
+    const uint32_t row = u >> log2;
+    piece = (int)(u & ((1u << log2) - 1));
     const uint32_t kv = row / heads;
     head = (int)(row - kv * heads);
     token = (int)(kv >> 1);
@@ -49,49 +61,118 @@ struct Unit {
   }
 };
 
+// The neighbour's value, a lane (or two) away in its group of four.
+template <int STEP>
+__device__ __forceinline__ float neighbour(float v) {
+  constexpr int kPerm = STEP == 1 ? 0xB1 : 0x4E;  // [1 0 3 2], [2 3 0 1]
+  return __uint_as_float(
+      (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), kPerm, 0xF, 0xF, true));
+}
+
+// The 16-point transform of a group that lies E elements to a lane, in the
+// order of fwht16 (steps 1, 2, 4, 8: the same sums).  at: the lane's first
+// element.
+template <int E>
+__device__ __forceinline__ void fwht_lanes(float (&t)[E], int at) {
+#pragma unroll
+  for (int h = 1; h < E && h < 16; h <<= 1)
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      if (j & h) continue;
+      const float u = t[j], v = t[j + h];
+      t[j] = u + v;
+      t[j + h] = u - v;
+    }
+  if constexpr (E < 16) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const float o = neighbour<1>(t[j]);
+      t[j] = at & E ? o - t[j] : t[j] + o;
+    }
+  }
+  if constexpr (E < 8) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const float o = neighbour<2>(t[j]);
+      t[j] = at & (2 * E) ? o - t[j] : t[j] + o;
+    }
+  }
+}
+
+template <int E>
+__device__ __forceinline__ void signs_of(float (&t)[E], uint32_t signs, int at) {
+#pragma unroll
+  for (int j = 0; j < E; ++j)
+    t[j] = __uint_as_float(__float_as_uint(t[j]) ^ ((signs >> ((at + j) & 15)) << 31));
+}
+
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
 template <int FMT, bool RHT, typename T>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
   constexpr int B = block_of<FMT>();
+  constexpr int E = 32 / sizeof(T);  // elements of a piece
+  constexpr int kLog2 = E == 16 ? 4 : 3;
   const int seq = blockIdx.y;
   const KvSeq sq = kv_seq(a.b, seq, a.c.page_log2);
-  const uint32_t blocks = a.c.dim / B;
-  const uint32_t per_token = 2u * a.c.heads * blocks;
-  const uint32_t u = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
-  const Unit at(u, a.c.heads, blocks);
-  if ((uint64_t)u >= (uint64_t)sq.n * per_token) return;
-  const int64_t pos = sq.pos + at.token;
-  if (pos < 0 || pos >= sq.kv) return;
-  const int64_t row = row_of(a.c, a.b, seq, (int)pos, at.head);
-  if (row < 0) return;
-  const T* x = (at.part ? static_cast<const T*>(a.x[1]) : static_cast<const T*>(a.x[0])) +
-               (sq.first + at.token) * (at.part ? a.token[1] : a.token[0]) +
-               at.head * (at.part ? a.head[1] : a.head[0]) + at.block * B;
-  RowRaw<T, B> raw;
-  raw.load(x);
-  float t[B], amax = 0.0f;
+  const int pieces_log2 = a.c.dim_log2 - kLog2;
+  const uint32_t units = (uint32_t)sq.n * 2u * a.c.heads << pieces_log2;
+  const uint32_t first = blockIdx.x * (uint32_t)(kThreads * kAppendPieces) + threadIdx.x;
+  if (first - threadIdx.x >= units) return;
+  u4 raw[kAppendPieces][2];
+  int64_t row[kAppendPieces];
 #pragma unroll
-  for (int g = 0; g < B / 16; ++g) {
-    float w[16];
-    raw.template group<RHT>(g, w, a.c.signs);
-    if constexpr (RHT) fwht16(w);
+  for (int k = 0; k < kAppendPieces; ++k) {
+    const uint32_t u = first + k * kThreads;
+    const Unit at(u < units ? u : 0u, a.c.heads, pieces_log2);
+    const int64_t pos = sq.pos + at.token;
+    row[k] = u < units && pos >= 0 && pos < sq.kv ? row_of(a.c, a.b, seq, (int)pos, at.head) : -1;
+    const T* x = (at.part ? static_cast<const T*>(a.x[1]) : static_cast<const T*>(a.x[0])) +
+                 (sq.first + at.token) * (at.part ? a.token[1] : a.token[0]) +
+                 at.head * (at.part ? a.head[1] : a.head[0]) + at.piece * E;
+    raw[k][0] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(x));
+    raw[k][1] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(x) + 1);
+  }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      t[16 * g + j] = w[j];
-      amax = fmaxf(amax, fabsf(w[j]));
+  for (int k = 0; k < kAppendPieces; ++k) {
+    // lanes of a block (and of a 16-group) take the same way
+    if (row[k] < 0) continue;
+    const Unit at(first + k * kThreads, a.c.heads, pieces_log2);
+    float t[E], amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t w = raw[k][j / 4][j % 4];
+      if constexpr (E == 16) {
+        t[2 * j] = __uint_as_float(w << 16);
+        t[2 * j + 1] = __uint_as_float(w & 0xFFFF0000u);
+      } else {
+        t[j] = __uint_as_float(w);
+      }
     }
+    if constexpr (RHT) {
+      signs_of(t, a.c.signs, at.piece * E);
+      fwht_lanes(t, at.piece * E);
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j) amax = fmaxf(amax, fabsf(t[j]));
+    if constexpr (B > E) amax = fmaxf(amax, neighbour<1>(amax));
+    if constexpr (B > 2 * E) amax = fmaxf(amax, neighbour<2>(amax));
+    ScaleCtx ctx{0.0f, 0.0f, 0.0f};
+    if constexpr (FMT == kNVFP4) {
+      ctx.s_t = at.part ? *a.c.v_scale : *a.c.k_scale;
+      ctx.den = ctx.s_t * grid_max<FMT>();
+    }
+    uint32_t packed[E / 8], sbyte;
+    encode_block<FMT, false, RHT, sizeof(T) == 2, E, kTsOuter>(t, amax, ctx, nullptr, 0u, 0u, 0u,
+                                                               packed, sbyte);
+    uint8_t* codes = (at.part ? a.c.v_codes : a.c.k_codes) + (row[k] << (a.c.dim_log2 - 1)) +
+                     at.piece * (E / 2);
+    if constexpr (E == 16) store8<false>(codes, packed[0], packed[1]);
+    else *reinterpret_cast<uint32_t*>(codes) = packed[0];
+    if (at.piece % (B / E) == 0)
+      (at.part ? a.c.v_scales : a.c.k_scales)[row[k] * (a.c.dim / B) + at.piece / (B / E)] =
+          (uint8_t)sbyte;
   }
-  ScaleCtx ctx{0.0f, 0.0f, 0.0f};
-  if constexpr (FMT == kNVFP4) {
-    ctx.s_t = at.part ? *a.c.v_scale : *a.c.k_scale;
-    ctx.den = ctx.s_t * grid_max<FMT>();
-  }
-  uint32_t packed[B / 8], sbyte;
-  encode_block<FMT, false, RHT, sizeof(T) == 2, B, kTsOuter>(t, amax, ctx, nullptr, 0u, 0u, 0u,
-                                                             packed, sbyte);
-  uint8_t* codes = (at.part ? a.c.v_codes : a.c.k_codes) + row * (a.c.dim / 2) + at.block * (B / 2);
-  if constexpr (B == 16) store8<false>(codes, packed[0], packed[1]);
-  else store16<false>(codes, packed[0], packed[1], packed[2], packed[3]);
-  ((at.part ? a.c.v_scales : a.c.k_scales))[row * blocks + at.block] = (uint8_t)sbyte;
 }
 
 struct GatherArgs {
@@ -101,60 +182,73 @@ struct GatherArgs {
   int64_t token, head;
 };
 
-__device__ __forceinline__ void store_group(float* p, const float (&t)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    store16<false>(p + 4 * i, __float_as_uint(t[4 * i]), __float_as_uint(t[4 * i + 1]),
-                   __float_as_uint(t[4 * i + 2]), __float_as_uint(t[4 * i + 3]));
-}
-
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void store_group(uint16_t* p, const float (&t)[16]) {
-  uint32_t w[8];
+__device__ __forceinline__ u4 out_of(const float (&t)[4]) {
+  return u4{__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]),
+            __float_as_uint(t[3])};
+}
+__device__ __forceinline__ u4 out_of(const float (&t)[8]) {
+  u4 w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const f32x2 v = {t[2 * i], t[2 * i + 1]};
     w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
   }
-  store16<false>(p, w[0], w[1], w[2], w[3]);
-  store16<false>(p + 8, w[4], w[5], w[6], w[7]);
+  return w;
 }
 
-// A lane reads one 16-element group: eight code bytes and its block's scale.
 template <int B, typename T>
 __global__ __launch_bounds__(kThreads) void kv_gather_kernel(GatherArgs a) {
+  constexpr int E = 16 / sizeof(T);  // elements of a piece
+  constexpr int kLog2 = E == 8 ? 3 : 2;
+  typedef typename std::conditional<E == 8, uint32_t, uint16_t>::type codes_t;
   const int seq = blockIdx.y;
   const KvSeq sq = kv_seq(a.b, seq, a.c.page_log2);
-  const uint32_t groups = a.c.dim / 16;
-  const uint32_t u = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
-  const Unit at(u, a.c.heads, groups);
-  if ((uint64_t)u >= (uint64_t)sq.n * (2u * a.c.heads * groups)) return;
-  const int64_t pos = sq.pos + at.token;
-  const int64_t row =
-      pos < 0 || pos >= sq.kv ? -1 : row_of(a.c, a.b, seq, (int)pos, at.head);
-  float t[16];
-  if (row < 0) {  // no such token in the cache: zeros
+  const int pieces_log2 = a.c.dim_log2 - kLog2;
+  const uint32_t units = (uint32_t)sq.n * 2u * a.c.heads << pieces_log2;
+  const uint32_t first = blockIdx.x * (uint32_t)(kThreads * kGatherPieces) + threadIdx.x;
+  if (first - threadIdx.x >= units) return;
+  uint32_t codes[kGatherPieces], scale[kGatherPieces];
+  bool held[kGatherPieces];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) t[j] = 0.0f;
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>((at.part ? a.c.v_codes : a.c.k_codes) +
-                                                    row * (a.c.dim / 2) + at.block * 8);
-    const uint32_t S = (at.part ? a.c.v_scales : a.c.k_scales)[row * (a.c.dim / B) +
-                                                               at.block * 16 / B];
+  for (int k = 0; k < kGatherPieces; ++k) {
+    const uint32_t u = first + k * kThreads;
+    const Unit at(u < units ? u : 0u, a.c.heads, pieces_log2);
+    const int64_t pos = sq.pos + at.token;
+    int64_t row = u < units && pos >= 0 && pos < sq.kv ? row_of(a.c, a.b, seq, (int)pos, at.head) : -1;
+    held[k] = row >= 0;
+    if (row < 0) row = 0;
+    codes[k] = *reinterpret_cast<const codes_t*>((at.part ? a.c.v_codes : a.c.k_codes) +
+                                                 (row << (a.c.dim_log2 - 1)) + at.piece * (E / 2));
+    scale[k] = (at.part ? a.c.v_scales : a.c.k_scales)[row * (a.c.dim / B) + at.piece * E / B];
+  }
+#pragma unroll
+  for (int k = 0; k < kGatherPieces; ++k) {
+    const uint32_t u = first + k * kThreads;
+    if (u >= units) return;  // whole rows: lanes of a 16-group take the same way
+    const Unit at(u, a.c.heads, pieces_log2);
     float d;
-    if constexpr (B == 16) d = (at.part ? *a.c.v_scale : *a.c.k_scale) * e4m3_decode(S);
-    else d = S ? __uint_as_float(S << 23) : 0x1p-127f;
+    if constexpr (B == 16) d = (at.part ? *a.c.v_scale : *a.c.k_scale) * e4m3_decode(scale[k]);
+    else d = scale[k] ? __uint_as_float(scale[k] << 23) : 0x1p-127f;
+    float t[E];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t c = ((j < 8 ? w.x : w.y) >> (4 * (j & 7))) & 15u;
+    for (int j = 0; j < E; ++j) {
+      const uint32_t c = (codes[k] >> (4 * j)) & 15u;
       const float v = e2m1_level(c & 7u) * d;
       t[j] = (c & 8u) ? -v : v;
     }
-    if (a.c.rht) rht16_inverse(t, a.c.signs);
+    if (a.c.rht) {
+      fwht_lanes(t, at.piece * E);
+#pragma unroll
+      for (int j = 0; j < E; ++j) t[j] *= 0.25f;
+      signs_of(t, a.c.signs, at.piece * E);
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j) t[j] = held[k] ? t[j] : 0.0f;  // no such token in the cache
+    T* out = static_cast<T*>(at.part ? a.out[1] : a.out[0]) + (sq.first + at.token) * a.token +
+             at.head * a.head + at.piece * E;
+    __builtin_nontemporal_store(out_of(t), reinterpret_cast<u4*>(out));
   }
-  T* out = static_cast<T*>(at.part ? a.out[1] : a.out[0]) + (sq.first + at.token) * a.token +
-           at.head * a.head + at.block * 16;
-  store_group(out, t);
 }
 
 template <int FMT, bool RHT>
@@ -162,6 +256,13 @@ hipError_t launch_append(const AppendArgs& a, int dtype, dim3 grid, hipStream_t 
   if (dtype == 0) kv_append_kernel<FMT, RHT, uint16_t><<<grid, kThreads, 0, s>>>(a);
   else kv_append_kernel<FMT, RHT, float><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
+}
+
+// Workgroups for the longest sequence's new tokens, in lanes of `pieces` of
+// `elements` each, and for all sequences.
+dim3 grid_of(const KvCacheArgs& c, const KvBatchArgs& b, int elements, int pieces) {
+  const int64_t units = (int64_t)b.max_q * 2 * c.heads * (c.dim / elements), n = kThreads * pieces;
+  return dim3((unsigned)((units + n - 1) / n), (unsigned)b.batch);
 }
 
 }  // namespace
@@ -176,9 +277,7 @@ hipError_t fp4_launch_kv_append(const KvAppendLaunch& q, hipStream_t s) {
   a.token[1] = q.v_token;
   a.head[0] = q.k_head;
   a.head[1] = q.v_head;
-  const int B = q.cache.format == kNVFP4 ? 16 : 32;
-  const int64_t units = (int64_t)q.batch.max_q * 2 * q.cache.heads * (q.cache.dim / B);
-  const dim3 grid((unsigned)((units + kThreads - 1) / kThreads), (unsigned)q.batch.batch);
+  const dim3 grid = grid_of(q.cache, q.batch, q.dtype == 0 ? 16 : 8, kAppendPieces);
   switch (q.cache.format) {
     case kNVFP4:
       return q.cache.rht ? launch_append<kNVFP4, true>(a, q.dtype, grid, s)
@@ -200,8 +299,7 @@ hipError_t fp4_launch_kv_gather(const KvGatherLaunch& q, hipStream_t s) {
   a.out[1] = q.v;
   a.token = q.token;
   a.head = q.head;
-  const int64_t units = (int64_t)q.batch.max_q * 2 * q.cache.heads * (q.cache.dim / 16);
-  const dim3 grid((unsigned)((units + kThreads - 1) / kThreads), (unsigned)q.batch.batch);
+  const dim3 grid = grid_of(q.cache, q.batch, q.dtype == 0 ? 8 : 4, kGatherPieces);
   const bool nv = q.cache.format == kNVFP4;
   if (q.dtype == 0) {
     if (nv) kv_gather_kernel<16, uint16_t><<<grid, kThreads, 0, s>>>(a);
