@@ -156,6 +156,7 @@ struct Args {
   float2* part_ml;
   uint32_t* starts;
   int splits, groups;
+  int pieces;     // few rows: of every segment; 0: dealt from the list
   int join_rows;  // rows of a row tile that the longest sequence fills
 };
 
@@ -291,10 +292,25 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // keeps the next R - 1 tiles on their way in registers (no depth or
 // occupancy beyond that changed the time), and the workgroups' equal runs
 // keep every compute unit reading to the end.
-constexpr int kFewThreads = 256, kFewWaves = 4, kFewKeys = 32, kFewLeast = 4;
+constexpr int kFewThreads = 256, kFewWaves = 4;
 
-// Tiles of a wave at work or on their way.
-__host__ __device__ constexpr int few_ring(int dim) { return dim == 64 ? 3 : 2; }
+// Keys of a tile.  (64 columns with 32 keys: 36 us in place of 32 for 48
+// sequences under a window of 4096, the chain of a tile's steps being as long.)
+__host__ __device__ constexpr int few_keys(int dim) { return dim == 64 ? 64 : 32; }
+
+constexpr int kFewRing = 2;  // tiles of a wave at work or on their way
+
+// How the tiles are dealt (fp4_plan_kv_attention).  Equal runs cost a
+// search of the list, a run's cuts and the joining, some 8 us, whatever the
+// lengths; equal pieces of every segment cost only the joining, but the
+// longest sequence sets the time; one piece needs no joining.  64 to 8192
+// keys, 8 key heads of 128 columns, one row tile, us for the three:
+//   1 sequence:    500 keys 15.2 / - / 10.5,  1500: 16.9 / 12.3 / 19,  6000: 18.1 / 15
+//   64 (ragged):   500 keys 23 / - / 13,  2000: 34 / - / 29,  4000: 47 / - / 49
+constexpr int kFewWhole = 20;  // tiles: one piece up to here
+constexpr int kFewPiece = 6;   // least tiles of a piece
+constexpr int kFewMost = 112;  // most tiles of a piece: beyond, equal runs
+constexpr int kFewRun = 4;     // least tiles of a run
 
 // Workgroups of a compute unit at once (registers and LDS set it).
 __host__ __device__ constexpr int few_residents(int dim, int rows) {
@@ -309,14 +325,15 @@ struct Few {
   static constexpr int W = C / 32;        // words of codes per lane and part = QK instructions
   static constexpr int J = C / 16;        // PV instructions (16 columns) of a part
   static constexpr int pitch = 2 * C + 16;  // of a V row in LDS, bytes (below)
+  static constexpr int K = few_keys(D), R = K / 16;  // keys of a tile, in rows of sixteen
 };
 
 template <bool MX, int D>
 struct FewTile {
   typedef Few<D> F;
-  uint32_t k[2][F::P][F::W], v[2][F::P][F::W];
-  uint32_t ks[2][F::P], vs[2][F::P];  // words with the scale bytes
-  int page[2];
+  uint32_t k[F::R][F::P][F::W], v[F::R][F::P][F::W];
+  uint32_t ks[F::R][F::P], vs[F::R][F::P];  // words with the scale bytes
+  int page[F::R];
 };
 
 template <int N>
@@ -351,7 +368,7 @@ __device__ __forceinline__ constexpr int scale_byte(int m, int g, int p) {
 }
 
 template <bool MX, int D>
-__device__ __forceinline__ void few_load(const Args& a, int h, int t0, const int (&page)[2],
+__device__ __forceinline__ void few_load(const Args& a, int h, int t0, const int (&page)[Few<D>::R],
                                          FewTile<MX, D>& x) {
   typedef Few<D> F;
   constexpr int B = MX ? 32 : 16;
@@ -359,7 +376,7 @@ __device__ __forceinline__ void few_load(const Args& a, int h, int t0, const int
   // a lane's place in sixteen rows: 32-bit offsets from wave-uniform bases
   const uint32_t code = m * (D / 2) + g * (F::C / 8);
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+  for (int r = 0; r < F::R; ++r) {
     x.page[r] = page[r];
     // sixteen tokens lie in one page; a page that the sequence does not have
     // is read as page 0 and its tokens are masked
@@ -403,7 +420,7 @@ __device__ __forceinline__ float max_over_g(float v) {
 template <bool LO, int D, int NT>
 struct FewLds {
   typedef Few<D> F;
-  static constexpr int v = kFewWaves * kFewKeys * F::pitch;
+  static constexpr int v = kFewWaves * F::K * F::pitch;
   static constexpr int o = kFewWaves * 16 * (F::C + 4) * 4;
   static constexpr int q = v > o ? v : o;
   static constexpr int q_part = NT * 16 * D * 2;  // high (or only) parts, then low parts
@@ -413,15 +430,16 @@ struct FewLds {
 };
 
 // The list of work: every row tile of every sequence ("entry": sequence-major)
-// and every key head of it ("segment") has some tiles of keys; the tiles of
-// all segments in order are dealt to the workgroups in equal runs, whatever
-// the lengths.  A workgroup walks its run segment by segment.  A segment that
-// lies in one run is written out; of one that does not, each piece goes to a
-// slot of its workgroup: 2 g for the piece that its run begins with, 2 g + 1
-// for one that begins later (only its run's last piece can be cut), and
-// kv_few_join_kernel joins the pieces in the order of the list.  (With the
-// keys cut into equal pieces per sequence instead, 64 sequences of 2048 to
-// 8192 keys took 102 us at the best number of pieces; so 81.)
+// and every key head of it ("segment") has some tiles of keys.  Short segments
+// are cut into a.pieces equal pieces each (at most their tiles), a workgroup
+// and a slot to a piece.  Longer ones (pieces 0) are dealt to the workgroups
+// in equal runs of the tiles of all segments in order, whatever the lengths;
+// a workgroup walks its run segment by segment.  A segment that lies in one
+// run is written out; of one that does not, each piece goes to a slot of its
+// workgroup: 2 g for the piece that its run begins with, 2 g + 1 for one that
+// begins later (only its run's last piece can be cut).  kv_few_join_kernel
+// joins the pieces in the order of the list.  (64 sequences of 2048 to 8192
+// keys in equal pieces took 102 us at the best number of them; so 81.)
 // The host keeps the number of tiles under 2^31.
 struct Runs {
   uint32_t per, more;  // tiles of a run; the first `more` runs have one more
@@ -439,11 +457,11 @@ struct Runs {
   }
 };
 
-template <int NT>
+template <int D, int NT>
 struct Entry {
   KvSeq s;
   int seq, r0, r1;  // rows [r0, r1) of the sequence; none if r0 >= r1
-  Keys<kFewKeys> keys;
+  Keys<few_keys(D)> keys;
   __device__ __forceinline__ void init(const Args& a, int e) {
     seq = e / a.row_tiles;
     s = kv_seq(a.b, seq, a.c.page_log2);
@@ -454,6 +472,11 @@ struct Entry {
     if (r0 < r1) keys.init(a, s, r0 / a.group, (r1 - 1) / a.group);
   }
 };
+
+// Pieces of a segment of n tiles, where every segment is cut by itself.
+__device__ __forceinline__ uint32_t pieces_of(const Args& a, uint32_t n) {
+  return n < (uint32_t)a.pieces ? n : (uint32_t)a.pieces;
+}
 
 // Sum over the lanes before this one, and over all (DPP moves: no LDS trip).
 __device__ __forceinline__ uint32_t wave_sum_before(uint32_t v, uint32_t& all) {
@@ -477,13 +500,13 @@ __device__ __forceinline__ int64_t readlane64(int64_t v, int l) {
 // Total tiles of the list, and the entry that holds the first tile of the
 // workgroup's run, with its number and the tiles before it.  Every wave does
 // this by itself, a lane per entry.
-template <int NT>
+template <int D, int NT>
 __device__ __forceinline__ void find_run(const Args& a, int entries, uint32_t& total, int& entry,
-                                         uint32_t& before, Entry<NT>& at) {
+                                         uint32_t& before, Entry<D, NT>& at) {
   const int lane = threadIdx.x & 63;
   total = 0;
   uint32_t mine = 0, ahead = 0, all;
-  Entry<NT> en;
+  Entry<D, NT> en;
   auto look = [&](int e) {
     mine = 0;
     if (e < entries) {
@@ -592,14 +615,14 @@ __device__ __forceinline__ void few_query(const Args& a, const KvSeq& s, int h, 
 
 // Tiles [first, end) of a segment, into its rows' outputs (slot < 0) or a slot.
 template <bool MX, bool LO, int D, int NT>
-__device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, int h, int first,
+__device__ __forceinline__ void few_piece(const Args& a, const Entry<D, NT>& en, int h, int first,
                                           int end, int64_t slot, uint8_t* lds) {
   typedef Num<MX> N;
   typedef typename N::x8 x8;
   typedef Few<D> F;
   typedef FewLds<LO, D, NT> L;
   const KvSeq& s = en.s;
-  const Keys<kFewKeys>& keys = en.keys;
+  const auto& keys = en.keys;
   const int seq = en.seq, r0 = en.r0, r1 = en.r1;
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -608,14 +631,14 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
   // next R - 1 are in flight.  The loads are unconditional (past the last
   // tile they read it again), so that the compiler can count them and wait
   // for the oldest alone.
-  constexpr int R = few_ring(D);
+  constexpr int R = kFewRing;
   FewTile<MX, D> ring[R];
   const int last = end - 1;
-  int page[2];
+  int page[F::R];
   auto pages_at = [&](int u) {
     const int t = keys.base(u < last ? u : last);
-    page[0] = page_of(a, seq, t, keys.hi);
-    page[1] = page_of(a, seq, t + 16, keys.hi);
+#pragma unroll
+    for (int r = 0; r < F::R; ++r) page[r] = page_of(a, seq, t + 16 * r, keys.hi);
   };
   int u = first + wave;
   pages_at(u);
@@ -656,7 +679,7 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
 
   // the lane's place in a store of V (its token's row, its quarter) and in a
   // transposing read (one of the four tokens of its lane group, four columns)
-  uint8_t* vt = lds + wave * (kFewKeys * F::pitch);
+  uint8_t* vt = lds + wave * (F::K * F::pitch);
   uint8_t* v_to = vt + m * F::pitch + g * (F::C / 2);
   const uint8_t* v_from = vt + (4 * g + (m >> 2)) * F::pitch + (m & 3) * 8;
   const uint8_t* q_from = lds + L::q + lane * 16;
@@ -666,7 +689,9 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
   const int64_t all_lo = a.window > 0 ? p1 + 1 - a.window : 0;
 
   auto work = [&](FewTile<MX, D>& cur, int t0) {
-    const bool inside = t0 + kFewKeys <= all_hi && t0 >= all_lo && cur.page[0] >= 0 && cur.page[1] >= 0;
+    bool inside = t0 + F::K <= all_hi && t0 >= all_lo;
+#pragma unroll
+    for (int r = 0; r < F::R; ++r) inside = inside && cur.page[r] >= 0;
     if (!inside) {
       // what no row sees may hold anything (it was never written, or its
       // page was given back): its codes and scales become zeros, so that
@@ -674,7 +699,7 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
       int tm = t0 + m;
       asm volatile("" : "+v"(tm));  // a branch: most tiles skip this
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < F::R; ++r) {
         const int t = tm + 16 * r;
         const bool ok = cur.page[r] >= 0 && t < keys.hi && (t >= keys.lo || t < a.sinks);
 #pragma unroll
@@ -686,9 +711,11 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
       }
     }
     // S^T = K q^T: register i of tile r: key t0 + 16 r + 4 g + i
-    f32x4 sc[NT][2];
+    f32x4 sc[NT][F::R];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = f32x4{};
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < F::R; ++r) sc[n][r] = f32x4{};
 #pragma unroll
     for (int p = 0; p < F::P; ++p) {
       const int shift = (scale_byte<MX, D>(m, g, p) & 3) * 8;
@@ -702,7 +729,7 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
           if constexpr (LO) ql[n] = as8<MX>(*reinterpret_cast<const w4*>(q + L::q_part));
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < F::R; ++r) {
           Scale<MX> k;
           block_scale(cur.ks[r][p] >> shift, block_of_word<MX>(j), k);
           const x8 kf = as8<MX>(dequant8(cur.k[r][p][j], k));
@@ -718,7 +745,7 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
       const int shift = (scale_byte<MX, D>(m, g, p) & 3) * 8;
       wave_lds_fence();
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < F::R; ++r)
 #pragma unroll
         for (int j = 0; j < F::W; ++j) {
           Scale<MX> k;
@@ -729,19 +756,19 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
     };
     store_v(0);
 
-    x8 pf[NT];
+    x8 pf[NT][F::R / 2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float v[8];
+      float v[4 * F::R];
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < F::R; ++r)
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[4 * r + i] = sc[n][r][i];
       if (!inside) {
         int tg = t0 + 4 * g;
         asm volatile("" : "+v"(tg));  // a branch: most tiles skip this
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < F::R; ++r)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int t = tg + 16 * r + i;
@@ -751,7 +778,7 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
       }
       float mx = v[0];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, v[i]);
+      for (int i = 1; i < 4 * F::R; ++i) mx = fmaxf(mx, v[i]);
       mx *= rs[n];
       // The maximum only has to keep exp2 in range: it is raised when a
       // score passes it by 2^8 (FP16 holds probabilities to 2^16), which
@@ -768,26 +795,32 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
           for (int j = 0; j < F::J; ++j) o[n][p][j] *= f;
       }
       const float sub = top[n] == -__builtin_inff() ? 0.0f : top[n];
-      w4 w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = pack2<MX>(__builtin_amdgcn_exp2f(__builtin_fmaf(v[2 * i], rs[n], -sub)),
-                         __builtin_amdgcn_exp2f(__builtin_fmaf(v[2 * i + 1], rs[n], -sub)));
-      pf[n] = as8<MX>(w);
-      l[n] = N::mma(ones, pf[n], l[n]);  // every register: the row's sum
+      for (int c = 0; c < F::R / 2; ++c) {
+        w4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = pack2<MX>(__builtin_amdgcn_exp2f(__builtin_fmaf(v[8 * c + 2 * i], rs[n], -sub)),
+                           __builtin_amdgcn_exp2f(__builtin_fmaf(v[8 * c + 2 * i + 1], rs[n], -sub)));
+        pf[n][c] = as8<MX>(w);
+        l[n] = N::mma(ones, pf[n][c], l[n]);  // every register: the row's sum
+      }
     }
-    // O^T += V^T P^T: contraction slots (g, i): key t0 + 4 g + i, then t0 +
-    // 16 + 4 g + i - 4
+    // O^T += V^T P^T: contraction slots (g, i) of 32 keys from t on: key t + 4 g +
+    // i, then t + 16 + 4 g + i - 4
 #pragma unroll
     for (int p = 0; p < F::P; ++p) {
       if (p) store_v(p);
 #pragma unroll
-      for (int j = 0; j < F::J; ++j) {
-        const w2 x = read_tr16(v_from + 32 * j), y = read_tr16(v_from + 32 * j + 16 * F::pitch);
-        const x8 vf = as8<MX>(w4{x.x, x.y, y.x, y.y});
+      for (int c = 0; c < F::R / 2; ++c)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][p][j] = N::mma(vf, pf[n], o[n][p][j]);
-      }
+        for (int j = 0; j < F::J; ++j) {
+          const uint8_t* v = v_from + 32 * j + 32 * c * F::pitch;
+          const w2 x = read_tr16(v), y = read_tr16(v + 16 * F::pitch);
+          const x8 vf = as8<MX>(w4{x.x, x.y, y.x, y.y});
+#pragma unroll
+          for (int n = 0; n < NT; ++n) o[n][p][j] = N::mma(vf, pf[n][c], o[n][p][j]);
+        }
     }
   };
   while (u < end) {
@@ -859,22 +892,39 @@ __device__ __forceinline__ void few_piece(const Args& a, const Entry<NT>& en, in
 template <bool MX, bool LO, int D, int NT>
 __global__ __launch_bounds__(kFewThreads, few_residents(D, 16 * NT)) void kv_few_kernel(Args a) {
   __shared__ __align__(16) uint8_t lds[FewLds<LO, D, NT>::bytes];
-  const int entries = a.b.batch * a.row_tiles;
-  uint32_t total, before;
+  int entries = a.b.batch * a.row_tiles;
   int e;
-  Entry<NT> en;
-  find_run<NT>(a, entries, total, e, before, en);
-  const Runs runs(total, a.groups);
-  const uint32_t x0 = runs.begin(blockIdx.x), x1 = runs.begin(blockIdx.x + 1);
-  uint32_t x = x0;
-  // Entries that see nothing have no tiles: the workgroup that ends the entry
-  // before them writes their zeros, the first one those at the beginning.
-  bool known = x < x1;
-  if (blockIdx.x == 0) {
-    if (e > 0 || !known) known = false, e = 0, before = 0;
-  } else if (!known) {
-    return;
+  uint32_t before, x0, x1;
+  Entry<D, NT> en;
+  bool known = true;
+  if (a.pieces) {
+    const uint32_t segment = blockIdx.x / a.pieces, p = blockIdx.x - segment * a.pieces;
+    e = segment / a.c.heads;
+    const uint32_t h = segment - e * a.c.heads;
+    entries = e + 1;
+    en.init(a, e);
+    const uint32_t n = en.keys.n, pieces = pieces_of(a, n);
+    if (n == 0 ? h + p > 0 : p >= pieces) return;
+    before = 0;
+    x0 = h * n + p * n / pieces;
+    x1 = h * n + (p + 1) * n / pieces;
+  } else {
+    uint32_t total;
+    find_run<D, NT>(a, entries, total, e, before, en);
+    const Runs runs(total, a.groups);
+    x0 = runs.begin(blockIdx.x);
+    x1 = runs.begin(blockIdx.x + 1);
+    // Entries that see nothing have no tiles: the workgroup that ends the
+    // entry before them writes their zeros, the first one those at the
+    // beginning.
+    known = x0 < x1;
+    if (blockIdx.x == 0) {
+      if (e > 0 || !known) known = false, e = 0, before = 0;
+    } else if (!known) {
+      return;
+    }
   }
+  uint32_t x = x0;
   for (; e < entries; ++e) {
     if (!known) en.init(a, e);
     known = false;
@@ -888,7 +938,9 @@ __global__ __launch_bounds__(kFewThreads, few_residents(D, 16 * NT)) void kv_few
     while (x < x1 && x - before < here) {
       const int h = (int)((x - before) / n), t = (int)((x - before) - h * n);
       const int len = (int)(x1 - x < n - t ? x1 - x : n - t);
-      const int64_t slot = len == (int)n ? -1 : 2 * (int64_t)blockIdx.x + (x != x0);
+      const int64_t slot = len == (int)n ? -1
+                           : a.pieces    ? (int64_t)blockIdx.x
+                                         : 2 * (int64_t)blockIdx.x + (x != x0);
       few_piece<MX, LO, D, NT>(a, en, h, t, t + len, slot, lds);
       x += len;
       if (x < x1) __syncthreads();  // the LDS of the joined waves is the next piece's
@@ -1448,25 +1500,41 @@ __global__ __launch_bounds__(64 * kFewJoinWaves) void kv_few_join_kernel(Args a)
   const int h = job / a.join_rows, row = job - h * a.join_rows;
   if (h >= a.c.heads) return;
   const int seq = e / a.row_tiles;
-  const KvSeq s = kv_seq(a.b, seq, a.c.page_log2);
-  const uint32_t total = a.starts[a.b.batch * a.row_tiles], begin = a.starts[e];
-  const uint32_t tiles = a.starts[e + 1] - begin;
   const int r = (e - seq * a.row_tiles) * (16 * NT) + row;
-  if (tiles == 0 || r >= s.n * a.group) return;
-  const Runs runs(total, a.groups);
-  const uint32_t n = tiles / a.c.heads, x = begin + h * n;
-  const int g0 = runs.of(x), g1 = runs.of(x + n - 1);
-  if (g0 == g1) return;  // one workgroup had it all
+  KvSeq s;
+  int64_t first, base;  // slots of the first piece, and of those after it (a step apart)
+  int n, step;
+  if (a.pieces) {
+    Entry<D, NT> en;
+    en.init(a, e);
+    s = en.s;
+    n = (int)pieces_of(a, en.keys.n);
+    if (n < 2 || r >= en.r1) return;
+    first = base = ((int64_t)e * a.c.heads + h) * a.pieces;
+    step = 1;
+  } else {
+    s = kv_seq(a.b, seq, a.c.page_log2);
+    const uint32_t total = a.starts[a.b.batch * a.row_tiles], begin = a.starts[e];
+    const uint32_t tiles = a.starts[e + 1] - begin;
+    if (tiles == 0 || r >= s.n * a.group) return;
+    const Runs runs(total, a.groups);
+    const uint32_t per = tiles / a.c.heads, x = begin + h * per;
+    const int g0 = runs.of(x);
+    n = runs.of(x + per - 1) - g0 + 1;
+    if (n == 1) return;  // one workgroup had it all
+    first = 2 * (int64_t)g0 + (runs.begin(g0) != x);
+    base = 2 * (int64_t)g0;
+    step = 2;
+  }
   const int c = lane % C, sl = lane / C;
-  const int64_t first = 2 * (int64_t)g0 + (runs.begin(g0) != x);
-  auto at = [&](int g) { return (g == g0 ? first : 2 * (int64_t)g) * (16 * NT) + row; };
+  auto at = [&](int g) { return (g == 0 ? first : base + step * g) * (16 * NT) + row; };
   float top = -__builtin_inff(), l = 0.0f;
-  for (int g = g0 + lane; g <= g1; g += 64) top = fmaxf(top, a.part_ml[at(g)].x);
+  for (int g = lane; g < n; g += 64) top = fmaxf(top, a.part_ml[at(g)].x);
   top = wave_max(top);
   const float sub = top == -__builtin_inff() ? 0.0f : top;
   f32x4 v = {};
 #pragma unroll 8  // loads in flight
-  for (int g = g0 + sl; g <= g1; g += SL) {
+  for (int g = sl; g < n; g += SL) {
     const int64_t p = at(g);
     const float2 q = a.part_ml[p];
     const float f = __builtin_amdgcn_exp2f(q.x - sub);
@@ -1510,7 +1578,7 @@ template <bool MX, bool LO, int D, int NT>
 hipError_t launch_few(const Args& a, hipStream_t s) {
   kv_few_kernel<MX, LO, D, NT><<<(unsigned)a.groups, kFewThreads, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.groups == 1) return e;
+  if (e != hipSuccess || !a.part) return e;
   const dim3 grid((unsigned)((a.c.heads * a.join_rows + kFewJoinWaves - 1) / kFewJoinWaves),
                   (unsigned)(a.b.batch * a.row_tiles));
   kv_few_join_kernel<MX, D, NT><<<grid, 64 * kFewJoinWaves, 0, s>>>(a);
@@ -1562,13 +1630,25 @@ KvAttentionPlan fp4_plan_kv_attention(const KvCacheArgs& c, const KvBatchArgs& b
     if (p.splits > 1) p.bytes = (size_t)(p.splits * b.tokens * q_heads) * ((size_t)c.dim * 4 + 8);
     return p;
   }
-  // as many workgroups as the chip holds at once; fewer where a run would be
-  // shorter than a tile for each wave
+  // equal pieces of every segment while they are short, else runs; as many
+  // workgroups as the chip holds at once, fewer where a run would be shorter
+  // than a tile for each wave
   const int64_t resident = 256 * few_residents(c.dim, p.rows);
-  const int64_t tiles = segments * (seen / kFewKeys + 2);
-  int64_t n = tiles / kFewLeast;
-  if (n > resident) n = resident;
+  const int64_t tiles = seen / few_keys(c.dim) + 2;
   p.splits = 1;
+  if (segments > 0) {
+    int64_t pieces = resident / segments;
+    if (pieces > tiles / kFewPiece) pieces = tiles / kFewPiece;
+    if (pieces < 1 || tiles <= kFewWhole) pieces = 1;
+    if (tiles <= kFewMost * pieces) {
+      p.pieces = (int)pieces;
+      p.groups = segments * pieces;
+      if (pieces > 1) p.bytes = (size_t)p.groups * p.rows * ((size_t)c.dim * 4 + 8);
+      return p;
+    }
+  }
+  int64_t n = segments * tiles / kFewRun;
+  if (n > resident) n = resident;
   p.groups = n < 1 ? 1 : n;
   if (p.groups > 1)
     p.bytes = (size_t)p.groups * 2 * p.rows * ((size_t)c.dim * 4 + 8) +
@@ -1596,15 +1676,16 @@ hipError_t fp4_launch_kv_attention(const KvAttentionLaunch& q, hipStream_t s) {
   a.lse = q.lse;
   a.splits = p.splits;
   a.groups = (int)p.groups;
+  a.pieces = p.pieces;
   a.row_tiles = p.row_tiles;
   const int64_t rows_of_tile = (int64_t)q.batch.max_q * a.group;
   a.join_rows = (int)(rows_of_tile < p.rows ? rows_of_tile : p.rows);
   if (p.bytes) {
     const int64_t rows = p.prompt ? (int64_t)p.splits * q.batch.tokens * q.q_heads
-                                  : p.groups * 2 * p.rows;
+                                  : p.groups * (p.pieces ? 1 : 2) * p.rows;
     a.part = static_cast<float*>(q.workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part + rows * q.cache.dim);
-    if (!p.prompt) a.starts = reinterpret_cast<uint32_t*>(a.part_ml + rows);
+    if (!p.prompt && !p.pieces) a.starts = reinterpret_cast<uint32_t*>(a.part_ml + rows);
   }
   if (q.cache.format == kNVFP4) return launch<false, false>(a, p, s);
   return q.cache.rht ? launch<true, true>(a, p, s) : launch<true, false>(a, p, s);
