@@ -906,8 +906,9 @@ __global__ __launch_bounds__(kFewThreads, few_residents(D, 16 * NT)) void kv_few
     const uint32_t n = en.keys.n, pieces = pieces_of(a, n);
     if (n == 0 ? h + p > 0 : p >= pieces) return;
     before = 0;
-    x0 = h * n + p * n / pieces;
-    x1 = h * n + (p + 1) * n / pieces;
+    // (64 bits: a max_kv that is too small can make pieces of any size)
+    x0 = h * n + (uint32_t)((uint64_t)p * n / pieces);
+    x1 = h * n + (uint32_t)((uint64_t)(p + 1) * n / pieces);
   } else {
     uint32_t total;
     find_run<D, NT>(a, entries, total, e, before, en);

@@ -67,6 +67,10 @@ class KVBatch(NamedTuple):
 _CACHE = struct.Struct("@iiiiiiQqPPPPPP")
 _BATCH = struct.Struct("@PqPPiiii")
 _FORMAT = {f: (fp4.FORMATS[f], fp4.BLOCK[f]) for f in KV_FORMATS}
+# (names that every call looks up)
+_Tensor, _uint8, _int32, _float32 = torch.Tensor, torch.uint8, torch.int32, torch.float32
+_DTYPES, _Q_DTYPES = fp4.DTYPES, (torch.bfloat16,)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def bind(L):
@@ -122,8 +126,8 @@ def _need(ok, msg):
 
 def _ints(t, name, dims=1, device=None):
     """Checks an int32 tensor on the device of that index (None: any)."""
-    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
-    if not (dev >= 0 and t.dtype is torch.int32 and t.dim() == dims
+    dev = t.get_device() if isinstance(t, _Tensor) else -1
+    if not (dev >= 0 and t.dtype is _int32 and t.dim() == dims
             and (t.is_contiguous() or t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1)):
         raise ValueError("%s must be a %d-D int32 device tensor with dense rows" % (name, dims))
     if device is not None and dev != device:
@@ -152,12 +156,12 @@ def _cache(c: KVCache):
         raise ValueError("the cache's arrays do not agree in shape")
     dev = kc.get_device()
     for t in (kc, ks, vc, vs):
-        if t.dtype is not torch.uint8 or not t.is_contiguous() or dev < 0 or t.get_device() != dev:
+        if t.dtype is not _uint8 or not t.is_contiguous() or dev < 0 or t.get_device() != dev:
             raise ValueError("the cache's arrays are dense uint8 tensors on one device")
     kp = vp = 0
     if fmt == "nvfp4":
         for t in (kf, vf):
-            if t is not None and not (t.dtype is torch.float32 and t.numel() == layers
+            if t is not None and not (t.dtype is _float32 and t.numel() == layers
                                       and t.is_contiguous() and t.get_device() == dev):
                 raise ValueError("k_scale and v_scale are float32 [layers] on the cache's device")
         kp, vp = kf.data_ptr() if kf is not None else 0, vf.data_ptr() if vf is not None else 0
@@ -181,7 +185,7 @@ def _batch(b: KVBatch, device):
 def _rows(t, name, heads, dim, dtypes, device):
     """The strides of a [tokens, heads, head_dim] tensor with a dense last
     dimension (of a dimension of one, none that matter), its tokens and heads."""
-    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    shape = t.shape if isinstance(t, _Tensor) else ()
     if len(shape) != 3 or shape[2] != dim or (heads and shape[1] != heads):
         raise ValueError("%s must be [tokens, %s, %d]" % (name, heads or "heads", dim))
     if t.dtype not in dtypes:
@@ -192,17 +196,17 @@ def _rows(t, name, heads, dim, dtypes, device):
     return (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0), shape[0], shape[1]
 
 
-def _empty(stream, shape, dtype, device, what):
+def _empty(stream, like, shape, dtype, what):
+    """A buffer on the device of `like`, for a call on `stream`."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     with fp4._Alloc(stream) as al:
-        return al.empty(shape, dtype, device, what)
+        return al.empty(shape, dtype, like.device, what)
 
 
-def _stream(stream):
-    if stream is None:  # the current device's current stream, without an object for it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return fp4._stream(stream)
+def _stream(stream, device):
+    """The handle: by default of the device's current stream, without an object for it."""
+    return _raw_stream(device) if stream is None else fp4._stream(stream)
 
 
 def _raise(st, name):
@@ -217,12 +221,12 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, batch: KVBatch, 
     projection, say) into their places in a layer."""
     c, _, heads, dim, dev = _cache(cache)
     b = _batch(batch, dev)
-    k0, k1, tokens, _ = _rows(k, "k", heads, dim, fp4.DTYPES, dev)
-    v0, v1, v_tokens, _ = _rows(v, "v", heads, dim, fp4.DTYPES, dev)
+    k0, k1, tokens, _ = _rows(k, "k", heads, dim, _DTYPES, dev)
+    v0, v1, v_tokens, _ = _rows(v, "v", heads, dim, _DTYPES, dev)
     dtype = k.dtype
     _need(tokens == v_tokens and dtype is v.dtype, "k and v must agree in shape and type")
     _raise(fp4.load().fp4_kv_append(c, layer, b, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1,
-                                    fp4.DTYPES[dtype], tokens, _stream(stream)), "fp4_kv_append")
+                                    _DTYPES[dtype], tokens, _stream(stream, dev)), "fp4_kv_append")
 
 
 def kv_gather(cache: KVCache, batch: KVBatch, tokens: int, layer: int = 0,
@@ -234,16 +238,16 @@ def kv_gather(cache: KVCache, batch: KVBatch, tokens: int, layer: int = 0,
     c, _, heads, dim, dev = _cache(cache)
     b = _batch(batch, dev)
     if out is None:
-        shape, device = (tokens, heads, dim), cache.k_codes.device
-        out = (_empty(stream, shape, out_dtype, device, "k"),
-               _empty(stream, shape, out_dtype, device, "v"))
+        shape = (tokens, heads, dim)
+        out = (_empty(stream, cache.k_codes, shape, out_dtype, "k"),
+               _empty(stream, cache.k_codes, shape, out_dtype, "v"))
     k, v = out
-    s = _rows(k, "out[0]", heads, dim, fp4.DTYPES, dev)
+    s = _rows(k, "out[0]", heads, dim, _DTYPES, dev)
     dtype = k.dtype
-    _need(s == _rows(v, "out[1]", heads, dim, fp4.DTYPES, dev) and dtype is v.dtype
+    _need(s == _rows(v, "out[1]", heads, dim, _DTYPES, dev) and dtype is v.dtype
           and s[2] == tokens, "the outputs must agree in shape, type and strides")
     _raise(fp4.load().fp4_kv_gather(c, layer, b, k.data_ptr(), v.data_ptr(), s[0], s[1],
-                                    fp4.DTYPES[dtype], tokens, _stream(stream)), "fp4_kv_gather")
+                                    _DTYPES[dtype], tokens, _stream(stream, dev)), "fp4_kv_gather")
     return k, v
 
 
@@ -268,25 +272,26 @@ def kv_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, layer: int = 0
     Rows of no sequence are not written."""
     c, _, _, dim, dev = _cache(cache)
     b = _batch(batch, dev)
-    q0, q1, tokens, q_heads = _rows(q, "q", 0, dim, (torch.bfloat16,), dev)
+    q0, q1, tokens, q_heads = _rows(q, "q", 0, dim, _Q_DTYPES, dev)
     if out is None:
-        out = _empty(stream, (tokens, q_heads, dim), out_dtype, q.device, "out")
-    o0, o1, out_tokens, _ = _rows(out, "out", q_heads, dim, fp4.DTYPES, dev)
+        out = _empty(stream, q, (tokens, q_heads, dim), out_dtype, "out")
+    o0, o1, out_tokens, _ = _rows(out, "out", q_heads, dim, _DTYPES, dev)
     _need(out_tokens == tokens, "out must have q's shape")
     if lse is not None:
-        _need(lse.dtype is torch.float32 and lse.shape == (tokens, q_heads)
+        _need(lse.dtype is _float32 and lse.shape == (tokens, q_heads)
               and lse.is_contiguous() and lse.get_device() == dev,
               "lse must be a dense float32 [tokens, q_heads] tensor on the cache's device")
     L = fp4.load()
     if workspace is None:
         n = L.fp4_kv_attention_workspace_bytes(c, b, q_heads, tokens, window, sinks)
         if n:
-            workspace = _empty(stream, n, torch.uint8, q.device, "the workspace")
+            workspace = _empty(stream, cache.k_codes, n, _uint8, "the workspace")
     _raise(L.fp4_kv_attention(
         c, layer, b, q.data_ptr(), q0, q1, q_heads, tokens,
         1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(),
-        fp4.DTYPES[out.dtype], o0, o1, fp4._ptr(lse), fp4._ptr(workspace), fp4._nbytes(workspace),
-        _stream(stream)), "fp4_kv_attention")
+        _DTYPES[out.dtype], o0, o1, lse.data_ptr() if lse is not None else None,
+        workspace.data_ptr() if workspace is not None else None, fp4._nbytes(workspace),
+        _stream(stream, dev)), "fp4_kv_attention")
     return out
 
 
@@ -314,7 +319,7 @@ def kv_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor,
         _ints(tokens, "tokens", 1, dev)
         _need(tokens.shape == src.shape, "tokens must be as long as src")
     _raise(fp4.load().fp4_kv_copy_pages(c, src.data_ptr(), dst.data_ptr(), fp4._ptr(tokens),
-                                        src.shape[0], _stream(stream)), "fp4_kv_copy_pages")
+                                        src.shape[0], _stream(stream, dev)), "fp4_kv_copy_pages")
 
 
 def kv_fork(cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
@@ -333,15 +338,14 @@ def kv_fork(cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor, refs: 
     _need(parents.shape == children.shape, "parents and children must be of one length")
     _need(refs.shape[0] == pages, "refs must have a count for every page")
     n = parents.shape[0]
-    device = cache.k_codes.device
     if failed is None:
-        failed = _empty(stream, 1, torch.int32, device, "failed")
+        failed = _empty(stream, refs, 1, _int32, "failed")
     _ints(failed, "failed", 1, dev)
     if workspace is None:
-        workspace = _empty(stream, 16 * max(n, 1), torch.uint8, device, "the workspace")
+        workspace = _empty(stream, cache.k_codes, 16 * max(n, 1), _uint8, "the workspace")
     _raise(fp4.load().fp4_kv_fork(c, *t, lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
                                   children.data_ptr(), n, failed.data_ptr(), workspace.data_ptr(),
-                                  fp4._nbytes(workspace), _stream(stream)), "fp4_kv_fork")
+                                  fp4._nbytes(workspace), _stream(stream, dev)), "fp4_kv_fork")
     return failed
 
 
@@ -355,7 +359,7 @@ def kv_free(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, se
     _ints(seqs, "seqs", 1, dev)
     _raise(fp4.load().fp4_kv_free(*t, lens.data_ptr(), refs.data_ptr(), refs.shape[0], page_size,
                                   seqs.data_ptr(), seqs.shape[0], window, sinks,
-                                  _stream(stream)), "fp4_kv_free")
+                                  _stream(stream, dev)), "fp4_kv_free")
 
 
 def kv_compact(cache: KVCache, page_table: torch.Tensor, refs: torch.Tensor,
@@ -368,17 +372,16 @@ def kv_compact(cache: KVCache, page_table: torch.Tensor, refs: torch.Tensor,
     c, pages, _, _, dev = _cache(cache)
     t = _tables(page_table, refs, dev)
     _need(refs.shape[0] == pages, "refs must have a count for every page")
-    device = cache.k_codes.device
     if place is None:
-        place = _empty(stream, pages, torch.int32, device, "place")
+        place = _empty(stream, refs, pages, _int32, "place")
     if used is None:
-        used = _empty(stream, 1, torch.int32, device, "used")
+        used = _empty(stream, refs, 1, _int32, "used")
     _ints(place, "place", 1, dev)
     _ints(used, "used", 1, dev)
     _need(place.shape[0] == pages, "place must have an id for every page")
     if workspace is None:
-        workspace = _empty(stream, 4 * (pages + 3), torch.uint8, device, "the workspace")
+        workspace = _empty(stream, cache.k_codes, 4 * (pages + 3), _uint8, "the workspace")
     _raise(fp4.load().fp4_kv_compact(c, *t, refs.data_ptr(), place.data_ptr(), used.data_ptr(),
                                      workspace.data_ptr(), fp4._nbytes(workspace),
-                                     _stream(stream)), "fp4_kv_compact")
+                                     _stream(stream, dev)), "fp4_kv_compact")
     return place, used
