@@ -14,10 +14,14 @@
 // that lies in two or four lanes is joined by DPP moves.  (A whole block to a
 // lane strides 128 bytes between lanes for FP32.)  A lane has a few pieces in
 // flight, so that the chain length -> page -> data is waited for once, and
-// what is not used again goes past the caches.  51535 tokens of eight FP32
-// heads of 128 columns (MXFP4: 0.48 GB each way) take 105 us to write and 116
-// to read back, 126 and 150 with a lane to a block; without the non-temporal
-// accesses 122 and 143.
+// what is not used again goes past the caches.  A piece's place is found once
+// and the division by the heads is a product: reading back was bound by the
+// vector unit before (105 us for what now takes 73).
+//
+// 51535 tokens of eight FP32 heads of 128 columns (MXFP4: 0.48 GB each way)
+// take 105 us to write (4.6 TB/s) and 73 us to read back (6.5); with a lane to
+// a block 126 and 150, without the non-temporal accesses 122 and 143.  Runs of
+// neighbouring tokens kept on one chiplet change nothing (105, 73 to 76).
 #include "fp4_kv.h"
 #include "fp4_quantize.h"
 
@@ -27,13 +31,29 @@ using namespace fp4kv;
 
 namespace {
 
-// Pieces of a lane, at once.  Writing: 115, 105, 106 us for one, two, four;
-// reading back: 153, 123, 116.  (Single tokens: 3.5, 3.6, 3.9 us of either.)
+// Pieces of a lane, at once.  Writing: 113, 105, 109, 105 us for one to four;
+// reading back: 84, 72, 74, 73 for two, four, six, eight.  (Single tokens: 3.5
+// to 3.9 and 3.2 to 4.2 us.)
 constexpr int kAppendPieces = 2, kGatherPieces = 4;
+
+// Division by the number of heads d: n / d = (n * m >> 32) >> s for n < 2^31,
+// with s = ceil(log2 d) - 1 and m = floor(2^(32 + s) / d) + 1.  m d exceeds
+// 2^(32 + s) by at most d <= 2^(s + 1), so the product exceeds its exact value
+// by less than 2^(32 + s) / d * (d / 2^32 * n / 2^s / 2) < one step of 1 / d.
+struct Heads {
+  uint32_t d, m;
+  int s;
+  explicit Heads(uint32_t heads) : d(heads), m(0), s(0) {
+    while ((2u << s) < d) ++s;
+    m = (uint32_t)((1ull << (32 + s)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t under(uint32_t n) const { return d == 1 ? n : __umulhi(n, m) >> s; }
+};
 
 struct AppendArgs {
   KvCacheArgs c;
   KvBatchArgs b;
+  Heads heads;
   const void* x[2];  // K, V
   int64_t token[2], head[2];
 };
@@ -51,11 +71,11 @@ __device__ __forceinline__ int64_t row_of(const KvCacheArgs& c, const KvBatchArg
 // (1 << log2 pieces).
 struct Unit {
   int token, part, head, piece;
-  __device__ __forceinline__ Unit(uint32_t u, uint32_t heads, int log2) {
+  __device__ __forceinline__ Unit(uint32_t u, const Heads& heads, int log2) {
     const uint32_t row = u >> log2;
     piece = (int)(u & ((1u << log2) - 1));
-    const uint32_t kv = row / heads;
-    head = (int)(row - kv * heads);
+    const uint32_t kv = heads.under(row);
+    head = (int)(row - kv * heads.d);
     token = (int)(kv >> 1);
     part = (int)(kv & 1);
   }
@@ -121,15 +141,18 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
   if (first - threadIdx.x >= units) return;
   u4 raw[kAppendPieces][2];
   int64_t row[kAppendPieces];
+  int part[kAppendPieces];
+  const int at_in = (threadIdx.x & ((1 << pieces_log2) - 1)) * E;  // the same for all pieces
 #pragma unroll
   for (int k = 0; k < kAppendPieces; ++k) {
     const uint32_t u = first + k * kThreads;
-    const Unit at(u < units ? u : 0u, a.c.heads, pieces_log2);
+    const Unit at(u < units ? u : 0u, a.heads, pieces_log2);
     const int64_t pos = sq.pos + at.token;
     row[k] = u < units && pos >= 0 && pos < sq.kv ? row_of(a.c, a.b, seq, (int)pos, at.head) : -1;
     const T* x = (at.part ? static_cast<const T*>(a.x[1]) : static_cast<const T*>(a.x[0])) +
                  (sq.first + at.token) * (at.part ? a.token[1] : a.token[0]) +
-                 at.head * (at.part ? a.head[1] : a.head[0]) + at.piece * E;
+                 at.head * (at.part ? a.head[1] : a.head[0]) + at_in;
+    part[k] = at.part;
     raw[k][0] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(x));
     raw[k][1] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(x) + 1);
   }
@@ -137,7 +160,6 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
   for (int k = 0; k < kAppendPieces; ++k) {
     // lanes of a block (and of a 16-group) take the same way
     if (row[k] < 0) continue;
-    const Unit at(first + k * kThreads, a.c.heads, pieces_log2);
     float t[E], amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -150,8 +172,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
       }
     }
     if constexpr (RHT) {
-      signs_of(t, a.c.signs, at.piece * E);
-      fwht_lanes(t, at.piece * E);
+      signs_of(t, a.c.signs, at_in);
+      fwht_lanes(t, at_in);
     }
 #pragma unroll
     for (int j = 0; j < E; ++j) amax = fmaxf(amax, fabsf(t[j]));
@@ -159,18 +181,18 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
     if constexpr (B > 2 * E) amax = fmaxf(amax, neighbour<2>(amax));
     ScaleCtx ctx{0.0f, 0.0f, 0.0f};
     if constexpr (FMT == kNVFP4) {
-      ctx.s_t = at.part ? *a.c.v_scale : *a.c.k_scale;
+      ctx.s_t = part[k] ? *a.c.v_scale : *a.c.k_scale;
       ctx.den = ctx.s_t * grid_max<FMT>();
     }
     uint32_t packed[E / 8], sbyte;
     encode_block<FMT, false, RHT, sizeof(T) == 2, E, kTsOuter>(t, amax, ctx, nullptr, 0u, 0u, 0u,
                                                                packed, sbyte);
-    uint8_t* codes = (at.part ? a.c.v_codes : a.c.k_codes) + (row[k] << (a.c.dim_log2 - 1)) +
-                     at.piece * (E / 2);
+    uint8_t* codes = (part[k] ? a.c.v_codes : a.c.k_codes) + (row[k] << (a.c.dim_log2 - 1)) +
+                     at_in / 2;
     if constexpr (E == 16) store8<false>(codes, packed[0], packed[1]);
     else *reinterpret_cast<uint32_t*>(codes) = packed[0];
-    if (at.piece % (B / E) == 0)
-      (at.part ? a.c.v_scales : a.c.k_scales)[row[k] * (a.c.dim / B) + at.piece / (B / E)] =
+    if (at_in % B == 0)
+      (part[k] ? a.c.v_scales : a.c.k_scales)[row[k] * (a.c.dim / B) + at_in / B] =
           (uint8_t)sbyte;
   }
 }
@@ -178,6 +200,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
 struct GatherArgs {
   KvCacheArgs c;
   KvBatchArgs b;
+  Heads heads;
   void* out[2];
   int64_t token, head;
 };
@@ -197,6 +220,22 @@ __device__ __forceinline__ u4 out_of(const float (&t)[8]) {
   return w;
 }
 
+// Levels of E codes.
+template <int E>
+__device__ __forceinline__ void levels(uint32_t codes, float (&t)[E]) {
+  auto two = [&](auto byte) {
+    const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, decltype(byte)::value);
+    t[2 * decltype(byte)::value] = v.x;
+    t[2 * decltype(byte)::value + 1] = v.y;
+  };
+  two(std::integral_constant<int, 0>{});
+  two(std::integral_constant<int, 1>{});
+  if constexpr (E == 8) {
+    two(std::integral_constant<int, 2>{});
+    two(std::integral_constant<int, 3>{});
+  }
+}
+
 template <int B, typename T>
 __global__ __launch_bounds__(kThreads) void kv_gather_kernel(GatherArgs a) {
   constexpr int E = 16 / sizeof(T);  // elements of a piece
@@ -209,45 +248,46 @@ __global__ __launch_bounds__(kThreads) void kv_gather_kernel(GatherArgs a) {
   const uint32_t first = blockIdx.x * (uint32_t)(kThreads * kGatherPieces) + threadIdx.x;
   if (first - threadIdx.x >= units) return;
   uint32_t codes[kGatherPieces], scale[kGatherPieces];
+  T* out[kGatherPieces];
+  int part[kGatherPieces];
   bool held[kGatherPieces];
+  const int at_in = (threadIdx.x & ((1 << pieces_log2) - 1)) * E;  // the same for all pieces
 #pragma unroll
   for (int k = 0; k < kGatherPieces; ++k) {
     const uint32_t u = first + k * kThreads;
-    const Unit at(u < units ? u : 0u, a.c.heads, pieces_log2);
+    const Unit at(u < units ? u : 0u, a.heads, pieces_log2);
     const int64_t pos = sq.pos + at.token;
     int64_t row = u < units && pos >= 0 && pos < sq.kv ? row_of(a.c, a.b, seq, (int)pos, at.head) : -1;
     held[k] = row >= 0;
     if (row < 0) row = 0;
+    part[k] = at.part;
+    out[k] = static_cast<T*>(at.part ? a.out[1] : a.out[0]) + (sq.first + at.token) * a.token +
+             at.head * a.head + at_in;
     codes[k] = *reinterpret_cast<const codes_t*>((at.part ? a.c.v_codes : a.c.k_codes) +
-                                                 (row << (a.c.dim_log2 - 1)) + at.piece * (E / 2));
-    scale[k] = (at.part ? a.c.v_scales : a.c.k_scales)[row * (a.c.dim / B) + at.piece * E / B];
+                                                 (row << (a.c.dim_log2 - 1)) + at_in / 2);
+    scale[k] = (at.part ? a.c.v_scales : a.c.k_scales)[row * (a.c.dim / B) + at_in / B];
   }
 #pragma unroll
   for (int k = 0; k < kGatherPieces; ++k) {
-    const uint32_t u = first + k * kThreads;
-    if (u >= units) return;  // whole rows: lanes of a 16-group take the same way
-    const Unit at(u, a.c.heads, pieces_log2);
+    if (first + k * kThreads >= units) return;  // whole rows: lanes of a 16-group take the same way
     float d;
-    if constexpr (B == 16) d = (at.part ? *a.c.v_scale : *a.c.k_scale) * e4m3_decode(scale[k]);
+    if constexpr (B == 16) d = (part[k] ? *a.c.v_scale : *a.c.k_scale) * e4m3_decode(scale[k]);
     else d = scale[k] ? __uint_as_float(scale[k] << 23) : 0x1p-127f;
-    float t[E];
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const uint32_t c = (codes[k] >> (4 * j)) & 15u;
-      const float v = e2m1_level(c & 7u) * d;
-      t[j] = (c & 8u) ? -v : v;
+    if (!held[k]) {  // no such token in the cache
+      codes[k] = 0;
+      d = 0.0f;
     }
+    float t[E];
+    levels(codes[k], t);
+#pragma unroll
+    for (int j = 0; j < E; ++j) t[j] *= d;
     if (a.c.rht) {
-      fwht_lanes(t, at.piece * E);
+      fwht_lanes(t, at_in);
 #pragma unroll
       for (int j = 0; j < E; ++j) t[j] *= 0.25f;
-      signs_of(t, a.c.signs, at.piece * E);
+      signs_of(t, held[k] ? a.c.signs : 0u, at_in);
     }
-#pragma unroll
-    for (int j = 0; j < E; ++j) t[j] = held[k] ? t[j] : 0.0f;  // no such token in the cache
-    T* out = static_cast<T*>(at.part ? a.out[1] : a.out[0]) + (sq.first + at.token) * a.token +
-             at.head * a.head + at.piece * E;
-    __builtin_nontemporal_store(out_of(t), reinterpret_cast<u4*>(out));
+    __builtin_nontemporal_store(out_of(t), reinterpret_cast<u4*>(out[k]));
   }
 }
 
@@ -268,9 +308,7 @@ dim3 grid_of(const KvCacheArgs& c, const KvBatchArgs& b, int elements, int piece
 }  // namespace
 
 hipError_t fp4_launch_kv_append(const KvAppendLaunch& q, hipStream_t s) {
-  AppendArgs a{};
-  a.c = q.cache;
-  a.b = q.batch;
+  AppendArgs a{q.cache, q.batch, Heads(q.cache.heads), {}, {}, {}};
   a.x[0] = q.k;
   a.x[1] = q.v;
   a.token[0] = q.k_token;
@@ -292,9 +330,7 @@ hipError_t fp4_launch_kv_append(const KvAppendLaunch& q, hipStream_t s) {
 }
 
 hipError_t fp4_launch_kv_gather(const KvGatherLaunch& q, hipStream_t s) {
-  GatherArgs a{};
-  a.c = q.cache;
-  a.b = q.batch;
+  GatherArgs a{q.cache, q.batch, Heads(q.cache.heads), {}, 0, 0};
   a.out[0] = q.k;
   a.out[1] = q.v;
   a.token = q.token;
