@@ -71,6 +71,7 @@ _FORMAT = {f: (fp4.FORMATS[f], fp4.BLOCK[f]) for f in KV_FORMATS}
 _Tensor, _uint8, _int32, _float32 = torch.Tensor, torch.uint8, torch.int32, torch.float32
 _DTYPES, _Q_DTYPES = fp4.DTYPES, (torch.bfloat16,)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_NO_WORKSPACE = -6  # FP4_ERR_WORKSPACE
 
 
 def bind(L):
@@ -204,6 +205,12 @@ def _empty(stream, like, shape, dtype, what):
         return al.empty(shape, dtype, like.device, what)
 
 
+def _dtype(t):
+    if t not in _DTYPES:
+        raise TypeError("outputs have one of the types %s" % (tuple(_DTYPES),))
+    return _DTYPES[t]
+
+
 def _stream(stream, device):
     """The handle: by default of the device's current stream, without an object for it."""
     return _raw_stream(device) if stream is None else fp4._stream(stream)
@@ -239,15 +246,18 @@ def kv_gather(cache: KVCache, batch: KVBatch, tokens: int, layer: int = 0,
     b = _batch(batch, dev)
     if out is None:
         shape = (tokens, heads, dim)
-        out = (_empty(stream, cache.k_codes, shape, out_dtype, "k"),
-               _empty(stream, cache.k_codes, shape, out_dtype, "v"))
-    k, v = out
-    s = _rows(k, "out[0]", heads, dim, _DTYPES, dev)
-    dtype = k.dtype
-    _need(s == _rows(v, "out[1]", heads, dim, _DTYPES, dev) and dtype is v.dtype
-          and s[2] == tokens, "the outputs must agree in shape, type and strides")
-    _raise(fp4.load().fp4_kv_gather(c, layer, b, k.data_ptr(), v.data_ptr(), s[0], s[1],
-                                    _DTYPES[dtype], tokens, _stream(stream, dev)), "fp4_kv_gather")
+        k = _empty(stream, cache.k_codes, shape, out_dtype, "k")
+        v = _empty(stream, cache.k_codes, shape, out_dtype, "v")
+        o0, o1, dtype = heads * dim, dim, _dtype(out_dtype)
+    else:
+        k, v = out
+        s = _rows(k, "out[0]", heads, dim, _DTYPES, dev)
+        dtype = k.dtype
+        _need(s == _rows(v, "out[1]", heads, dim, _DTYPES, dev) and dtype is v.dtype
+              and s[2] == tokens, "the outputs must agree in shape, type and strides")
+        o0, o1, dtype = s[0], s[1], _DTYPES[dtype]
+    _raise(fp4.load().fp4_kv_gather(c, layer, b, k.data_ptr(), v.data_ptr(), o0, o1, dtype, tokens,
+                                    _stream(stream, dev)), "fp4_kv_gather")
     return k, v
 
 
@@ -275,23 +285,28 @@ def kv_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, layer: int = 0
     q0, q1, tokens, q_heads = _rows(q, "q", 0, dim, _Q_DTYPES, dev)
     if out is None:
         out = _empty(stream, q, (tokens, q_heads, dim), out_dtype, "out")
-    o0, o1, out_tokens, _ = _rows(out, "out", q_heads, dim, _DTYPES, dev)
-    _need(out_tokens == tokens, "out must have q's shape")
+        o0, o1, dtype = q_heads * dim, dim, _dtype(out_dtype)
+    else:
+        o0, o1, out_tokens, _ = _rows(out, "out", q_heads, dim, _DTYPES, dev)
+        _need(out_tokens == tokens, "out must have q's shape")
+        dtype = _DTYPES[out.dtype]
     if lse is not None:
         _need(lse.dtype is _float32 and lse.shape == (tokens, q_heads)
               and lse.is_contiguous() and lse.get_device() == dev,
               "lse must be a dense float32 [tokens, q_heads] tensor on the cache's device")
     L = fp4.load()
-    if workspace is None:
+    args = (c, layer, b, q.data_ptr(), q0, q1, q_heads, tokens,
+            1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), dtype,
+            o0, o1, lse.data_ptr() if lse is not None else None)
+    if workspace is None:  # most short calls need none: ask only if this one does
+        st = L.fp4_kv_attention(*args, None, 0, _stream(stream, dev))
+        if st != _NO_WORKSPACE:
+            _raise(st, "fp4_kv_attention")
+            return out
         n = L.fp4_kv_attention_workspace_bytes(c, b, q_heads, tokens, window, sinks)
-        if n:
-            workspace = _empty(stream, cache.k_codes, n, _uint8, "the workspace")
-    _raise(L.fp4_kv_attention(
-        c, layer, b, q.data_ptr(), q0, q1, q_heads, tokens,
-        1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(),
-        _DTYPES[out.dtype], o0, o1, lse.data_ptr() if lse is not None else None,
-        workspace.data_ptr() if workspace is not None else None, fp4._nbytes(workspace),
-        _stream(stream, dev)), "fp4_kv_attention")
+        workspace = _empty(stream, cache.k_codes, n, _uint8, "the workspace")
+    _raise(L.fp4_kv_attention(*args, workspace.data_ptr(), fp4._nbytes(workspace),
+                              _stream(stream, dev)), "fp4_kv_attention")
     return out
 
 
