@@ -10,8 +10,8 @@
 // Bound by bytes: 2 * D * element size read and 2 * (D / 2 + D / B) written
 // per token and head (2.28 times less out than in for BF16 NVFP4), or the
 // reverse.  Writing takes 32 bytes of a row in a lane, reading back gives 16:
-// consecutive lanes then touch consecutive bytes, and a block or 16-group
-// that lies in two or four lanes is joined by DPP moves.  (A whole block to a
+// consecutive lanes touch consecutive bytes, and a block or 16-group that
+// lies in two or four lanes is joined by DPP moves.  (A whole block to a
 // lane strides 128 bytes between lanes for FP32.)  A lane has a few pieces in
 // flight, so that the chain length -> page -> data is waited for once, and
 // what is not used again goes past the caches.  A piece's place is found once
@@ -19,9 +19,11 @@
 // vector unit before (105 us for what now takes 73).
 //
 // 51535 tokens of eight FP32 heads of 128 columns (MXFP4: 0.48 GB each way)
-// take 105 us to write (4.6 TB/s) and 73 us to read back (6.5); with a lane to
-// a block 126 and 150, without the non-temporal accesses 122 and 143.  Runs of
-// neighbouring tokens kept on one chiplet change nothing (105, 73 to 76).
+// take 94 us to write (5.1 TB/s) and 73 us to read back (6.5); with a lane to
+// a block 126 and 150.  Writing with each lane's 32 bytes loaded in place (two
+// loads that touch every other 16 bytes) took 105 us, 122 without the
+// non-temporal loads; runs of neighbouring tokens kept on one chiplet change
+// nothing.
 #include "fp4_kv.h"
 #include "fp4_quantize.h"
 
@@ -31,15 +33,15 @@ using namespace fp4kv;
 
 namespace {
 
-// Pieces of a lane, at once.  Writing: 113, 105, 109, 105 us for one to four;
-// reading back: 84, 72, 74, 73 for two, four, six, eight.  (Single tokens: 3.5
-// to 3.9 and 3.2 to 4.2 us.)
+// Pieces of a lane, at once.  Writing (before the loads were swapped between
+// lanes): 113, 105, 109, 105 us for one to four; reading back: 84, 72, 74, 73
+// for two, four, six, eight.  (Single tokens: 3.5 to 3.9 and 3.2 to 4.2 us.)
 constexpr int kAppendPieces = 2, kGatherPieces = 4;
 
 // Division by the number of heads d: n / d = (n * m >> 32) >> s for n < 2^31,
-// with s = ceil(log2 d) - 1 and m = floor(2^(32 + s) / d) + 1.  m d exceeds
-// 2^(32 + s) by at most d <= 2^(s + 1), so the product exceeds its exact value
-// by less than 2^(32 + s) / d * (d / 2^32 * n / 2^s / 2) < one step of 1 / d.
+// with s = ceil(log2 d) - 1 and m = floor(2^(32 + s) / d) + 1.  With e = m d -
+// 2^(32 + s), 0 < e <= d <= 2^(s + 1): n m / 2^(32 + s) = n / d + n e / (d
+// 2^(32 + s)), whose last term is below 1 / d, so the floor is that of n / d.
 struct Heads {
   uint32_t d, m;
   int s;
@@ -81,18 +83,27 @@ struct Unit {
   }
 };
 
-// The neighbour's value, a lane (or two) away in its group of four.
-template <int STEP>
-__device__ __forceinline__ float neighbour(float v) {
-  constexpr int kPerm = STEP == 1 ? 0xB1 : 0x4E;  // [1 0 3 2], [2 3 0 1]
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
   return __uint_as_float(
-      (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), kPerm, 0xF, 0xF, true));
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
 
-// The 16-point transform of a group that lies E elements to a lane, in the
-// order of fwht16 (steps 1, 2, 4, 8: the same sums).  at: the lane's first
-// element.
-template <int E>
+// The value of the lane that is STEP (1, 2 or 4) away, lane ^ STEP.
+template <int STEP>
+__device__ __forceinline__ float neighbour(float v) {
+  if constexpr (STEP == 1) return dpp<0xB1>(v);  // quad_perm [1 0 3 2]
+  else if constexpr (STEP == 2) return dpp<0x4E>(v);  // quad_perm [2 3 0 1]
+  else {
+    const float up = dpp<0x104>(v), down = dpp<0x114>(v);  // row_shl 4, row_shr 4
+    return threadIdx.x & 4 ? down : up;
+  }
+}
+
+// The 16-point transform of a group that lies E elements to a lane, in lanes
+// L apart, in the order of fwht16 (steps 1, 2, 4, 8: the same sums).  at: the
+// lane's first element.
+template <int L, int E>
 __device__ __forceinline__ void fwht_lanes(float (&t)[E], int at) {
 #pragma unroll
   for (int h = 1; h < E && h < 16; h <<= 1)
@@ -106,14 +117,14 @@ __device__ __forceinline__ void fwht_lanes(float (&t)[E], int at) {
   if constexpr (E < 16) {
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const float o = neighbour<1>(t[j]);
+      const float o = neighbour<L>(t[j]);
       t[j] = at & E ? o - t[j] : t[j] + o;
     }
   }
   if constexpr (E < 8) {
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const float o = neighbour<2>(t[j]);
+      const float o = neighbour<2 * L>(t[j]);
       t[j] = at & (2 * E) ? o - t[j] : t[j] + o;
     }
   }
@@ -139,22 +150,42 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
   const uint32_t units = (uint32_t)sq.n * 2u * a.c.heads << pieces_log2;
   const uint32_t first = blockIdx.x * (uint32_t)(kThreads * kAppendPieces) + threadIdx.x;
   if (first - threadIdx.x >= units) return;
+  // A wave's 64 pieces of 32 bytes are loaded as two runs of 1024, sixteen
+  // bytes to a lane; lane pairs then swap halves, so that the even lanes have
+  // the pieces of the first run and the odd ones those of the second.
   u4 raw[kAppendPieces][2];
   int64_t row[kAppendPieces];
-  int part[kAppendPieces];
-  const int at_in = (threadIdx.x & ((1 << pieces_log2) - 1)) * E;  // the same for all pieces
+  int part[kAppendPieces], at_in[kAppendPieces];
+  const bool odd = threadIdx.x & 1;
 #pragma unroll
   for (int k = 0; k < kAppendPieces; ++k) {
-    const uint32_t u = first + k * kThreads;
-    const Unit at(u < units ? u : 0u, a.heads, pieces_log2);
-    const int64_t pos = sq.pos + at.token;
-    row[k] = u < units && pos >= 0 && pos < sq.kv ? row_of(a.c, a.b, seq, (int)pos, at.head) : -1;
-    const T* x = (at.part ? static_cast<const T*>(a.x[1]) : static_cast<const T*>(a.x[0])) +
-                 (sq.first + at.token) * (at.part ? a.token[1] : a.token[0]) +
-                 at.head * (at.part ? a.head[1] : a.head[0]) + at_in;
-    part[k] = at.part;
-    raw[k][0] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(x));
-    raw[k][1] = __builtin_nontemporal_load(reinterpret_cast<const u4*>(x) + 1);
+    const uint32_t u = (first & ~63u) + k * kThreads + (threadIdx.x & 63) / 2;
+    const Unit a0(u < units ? u : 0u, a.heads, pieces_log2);
+    const Unit a1(u + 32 < units ? u + 32 : 0u, a.heads, pieces_log2);
+    auto load = [&](const Unit& at) {
+      const T* x = (at.part ? static_cast<const T*>(a.x[1]) : static_cast<const T*>(a.x[0])) +
+                   (sq.first + at.token) * (at.part ? a.token[1] : a.token[0]) +
+                   at.head * (at.part ? a.head[1] : a.head[0]) + at.piece * E;
+      return __builtin_nontemporal_load(reinterpret_cast<const u4*>(x) + (odd ? 1 : 0));
+    };
+    raw[k][0] = load(a0);
+    raw[k][1] = load(a1);
+    const int64_t pos = sq.pos + (odd ? a1.token : a0.token);
+    part[k] = odd ? a1.part : a0.part;
+    at_in[k] = (odd ? a1.piece : a0.piece) * E;
+    row[k] = (odd ? u + 32 : u) < units && pos >= 0 && pos < sq.kv
+                 ? row_of(a.c, a.b, seq, (int)pos, odd ? a1.head : a0.head)
+                 : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < kAppendPieces; ++k) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t give = odd ? raw[k][0][e] : raw[k][1][e];
+      const uint32_t get = __float_as_uint(neighbour<1>(__uint_as_float(give)));
+      raw[k][0][e] = odd ? get : raw[k][0][e];
+      raw[k][1][e] = odd ? raw[k][1][e] : get;
+    }
   }
 #pragma unroll
   for (int k = 0; k < kAppendPieces; ++k) {
@@ -172,13 +203,13 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
       }
     }
     if constexpr (RHT) {
-      signs_of(t, a.c.signs, at_in);
-      fwht_lanes(t, at_in);
+      signs_of(t, a.c.signs, at_in[k]);
+      fwht_lanes<2>(t, at_in[k]);
     }
 #pragma unroll
     for (int j = 0; j < E; ++j) amax = fmaxf(amax, fabsf(t[j]));
-    if constexpr (B > E) amax = fmaxf(amax, neighbour<1>(amax));
-    if constexpr (B > 2 * E) amax = fmaxf(amax, neighbour<2>(amax));
+    if constexpr (B > E) amax = fmaxf(amax, neighbour<2>(amax));
+    if constexpr (B > 2 * E) amax = fmaxf(amax, neighbour<4>(amax));
     ScaleCtx ctx{0.0f, 0.0f, 0.0f};
     if constexpr (FMT == kNVFP4) {
       ctx.s_t = part[k] ? *a.c.v_scale : *a.c.k_scale;
@@ -188,11 +219,11 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
     encode_block<FMT, false, RHT, sizeof(T) == 2, E, kTsOuter>(t, amax, ctx, nullptr, 0u, 0u, 0u,
                                                                packed, sbyte);
     uint8_t* codes = (part[k] ? a.c.v_codes : a.c.k_codes) + (row[k] << (a.c.dim_log2 - 1)) +
-                     at_in / 2;
+                     at_in[k] / 2;
     if constexpr (E == 16) store8<false>(codes, packed[0], packed[1]);
     else *reinterpret_cast<uint32_t*>(codes) = packed[0];
-    if (at_in % B == 0)
-      (part[k] ? a.c.v_scales : a.c.k_scales)[row[k] * (a.c.dim / B) + at_in / B] =
+    if (at_in[k] % B == 0)
+      (part[k] ? a.c.v_scales : a.c.k_scales)[row[k] * (a.c.dim / B) + at_in[k] / B] =
           (uint8_t)sbyte;
   }
 }
@@ -282,7 +313,7 @@ __global__ __launch_bounds__(kThreads) void kv_gather_kernel(GatherArgs a) {
 #pragma unroll
     for (int j = 0; j < E; ++j) t[j] *= d;
     if (a.c.rht) {
-      fwht_lanes(t, at_in);
+      fwht_lanes<1>(t, at_in);
 #pragma unroll
       for (int j = 0; j < E; ++j) t[j] *= 0.25f;
       signs_of(t, held[k] ? a.c.signs : 0u, at_in);
