@@ -961,14 +961,18 @@ __global__ __launch_bounds__(kFewThreads, few_residents(D, 16 * NT)) void kv_few
 // Waves of 32 rows each (eight of them, four for 256 columns) share tiles of
 // 64 keys, dequantized once into LDS (K and V, 16 bits, two tiles of each).
 //
-// Bound by issue: a score costs 4 * D matrix flops and about nine vector
-// instructions with the staging's share, one of them a quarter-rate exp2, so
-// the vector unit is as busy as the matrix unit.  Three steps of the work run
-// side by side on sub-tiles of 32 keys, in an order that is written out: the
-// scores of the next, the exponentials of this, the output of the one before,
-// with one barrier a tile.  Two waves to a SIMD fill each other's gaps (one,
-// of 64 rows, halves the LDS reads but leaves every wait open: 454 us for two
-// prompts of 4096 tokens against 384); of 256 columns only one fits.
+// Two prompts of 4096 tokens, 32 query and 8 key heads of 128 columns (NVFP4):
+// 312 us, 880 TFLOP/s of the pairs seen (a library product of 8192^3 reaches
+// 1485).  No unit is full: matrix instructions are busy 39 % of the time, the
+// vector unit 49 % (a score costs about nine vector instructions with the
+// staging's share), LDS 32 % (every fragment of 1 KB feeds one instruction);
+// the rest is waiting on one another.  So three steps of the work run side by
+// side on sub-tiles of 32 keys, in an order that is written out: the scores of
+// the next, the exponentials of this, the output of the one before, with one
+// barrier a tile.  Two waves to a SIMD fill some of each other's gaps (one, of
+// 64 rows, halves the LDS reads but leaves every wait open: 454 us under the
+// tracer against 384; two workgroups of four waves dequantize twice as much: 327
+// us back to back against 321); of 256 columns only one fits.
 constexpr int kManyKeys = 64;
 
 __host__ __device__ constexpr int many_waves(int dim) { return dim <= 128 ? 8 : 4; }
